@@ -89,6 +89,15 @@ def _load():
     L.kv2_attention_chunk.restype = I
     L.kv2_attention_chunk.argtypes = [ctypes.POINTER(kv2_cache), I, P, I, I, P, P, I,
                                       ctypes.c_float, P, I, P, S, P]
+    C, F = ctypes.POINTER(kv2_cache), ctypes.c_float
+    L.kv2_attention_cross_workspace_size.restype = S
+    L.kv2_attention_cross_workspace_size.argtypes = [C, I, I, I]
+    L.kv2_attention_cross.restype = I
+    L.kv2_attention_cross.argtypes = [C, P, I, P, P, I, I, F, P, I, P, S, P]
+    L.kv2_attention_shared_workspace_size.restype = S
+    L.kv2_attention_shared_workspace_size.argtypes = [C, C, I, I, I]
+    L.kv2_attention_shared.restype = I
+    L.kv2_attention_shared.argtypes = [C, P, I, C, P, I, P, I, F, P, I, P, S, P]
     L.kv2_page_bytes.restype = S
     L.kv2_page_bytes.argtypes = [ctypes.POINTER(kv2_cache)]
     L.kv2_page_store.restype = I
@@ -123,6 +132,8 @@ EXPORTS = ["kv2_status_string", "kv2_last_error", "kv2_version", "kv2_fit_worksp
            "kv2_attention_decode", "kv2_attention_decode_noalloc", "kv2_decode_noalloc_error",
            "kv2_append_attention_decode",
            "kv2_chunk_workspace_size", "kv2_attention_chunk",
+           "kv2_attention_cross_workspace_size", "kv2_attention_cross",
+           "kv2_attention_shared_workspace_size", "kv2_attention_shared",
            "kv2_page_bytes", "kv2_page_store", "kv2_page_load"]
 
 
@@ -394,6 +405,107 @@ def kv2_attention_chunk(cache: Cache, length: int, Q: torch.Tensor, Kself: torch
     _check(_get_lib().kv2_attention_chunk(ctypes.byref(d), length, _ptr(Q), H_q, Nq, _ptr(Kself), _ptr(Vself),
                                    frame_tokens, float(sm_scale), _ptr(out), out_dtype, _ptr(ws),
                                    ws.numel(), _stream(stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------
+# rows of queries: cross attention, decode over a shared prefix
+# ----------------------------------------------------------------------------
+
+def _need(name, t, shape, dtypes, device):
+    """A call's tensor: shape, element type, contiguous, on the call's device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(x) for x in dtypes)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+_BITS16 = (torch.bfloat16, torch.int16)
+
+
+def _rows_call(Q, shape, out_dtype, out, ws, need):
+    """Output and workspace of a row attention call (made when not passed)."""
+    if out_dtype not in (KV2_OUT_F32, KV2_OUT_BF16):
+        raise ValueError(f"out_dtype {out_dtype}")
+    want = torch.float32 if out_dtype == KV2_OUT_F32 else torch.bfloat16
+    if out is None:
+        out = torch.zeros(shape, dtype=want, device=Q.device)
+    _need("out", out, shape, (want,), Q.device)
+    if ws is None:
+        # zeroed: the first word is the sticky error word of device-side waits
+        ws = torch.zeros(max(need, 16), dtype=torch.uint8, device=Q.device)
+    return out, ws
+
+
+def kv2_attention_cross_workspace_size(cache: Cache, H_q: int, Nq: int, max_len: int) -> int:
+    d = cache.desc()
+    return int(_get_lib().kv2_attention_cross_workspace_size(ctypes.byref(d), H_q, Nq, max_len))
+
+
+def kv2_attention_cross(cache: Cache, lens, Q: torch.Tensor, sm_scale: float, out_dtype: int = KV2_OUT_F32,
+                        q_lens=None, max_len=None, out=None, ws=None, stream=None):
+    """Q bf16 [B][Nq][H_q][d] against the first lens[b] cached tokens of every
+    sequence, all of them visible to every query -> out of Q's shape (fp32 or
+    bf16). lens, q_lens: int32 [B] on the device (None: max_len tokens / Nq
+    queries each); max_len bounds lens (None: the cache's capacity). Rows of
+    ``out`` at or after q_lens[b] are left as they are."""
+    if Q.dim() != 4:
+        raise ValueError(f"Q: {Q.dim()} dimensions, expected [B][Nq][H_q][d]")
+    B, Nq, H_q, _ = Q.shape
+    dev = cache.k_code.device
+    _need("Q", Q, (cache.B, Nq, H_q, cache.d), _BITS16, dev)
+    for name, t in (("lens", lens), ("q_lens", q_lens)):
+        if t is not None:
+            _need(name, t, (B,), (torch.int32,), dev)
+    max_len = cache.capacity if max_len is None else int(max_len)
+    with torch.cuda.device(dev):
+        need = kv2_attention_cross_workspace_size(cache, H_q, Nq, max_len) if ws is None else 0
+        out, ws = _rows_call(Q, Q.shape, out_dtype, out, ws, need)
+        d = cache.desc()
+        _check(_get_lib().kv2_attention_cross(ctypes.byref(d), _ptr(lens), max_len, _ptr(Q), _ptr(q_lens), Nq, H_q,
+                                              float(sm_scale), _ptr(out), out_dtype, _ptr(ws), ws.numel(),
+                                              _stream(stream)))
+    return out
+
+
+def kv2_attention_shared_workspace_size(prefix: Cache, cache: Cache, H_q: int, max_prefix_len: int,
+                                        max_len: int) -> int:
+    p, d = prefix.desc(), cache.desc()
+    return int(_get_lib().kv2_attention_shared_workspace_size(ctypes.byref(p), ctypes.byref(d), H_q, max_prefix_len,
+                                                              max_len))
+
+
+def kv2_attention_shared(prefix: Cache, prefix_lens, cache: Cache, lens, Q: torch.Tensor, sm_scale: float,
+                         out_dtype: int = KV2_OUT_F32, max_prefix_len=None, max_len=None, out=None, ws=None,
+                         stream=None):
+    """Decode of cache.B sequences in prefix.B equal groups: Q bf16
+    [B][H_q][d] of sequence b attends to the first prefix_lens[b // (B /
+    prefix.B)] tokens of its group's prefix, then to the first lens[b] of its
+    own cache -> out [B][H_q][d]. Lengths: int32 on the device (None: the
+    maxima); the maxima bound them (None: the capacities)."""
+    if Q.dim() != 3:
+        raise ValueError(f"Q: {Q.dim()} dimensions, expected [B][H_q][d]")
+    B, H_q, _ = Q.shape
+    dev = cache.k_code.device
+    _need("Q", Q, (cache.B, H_q, cache.d), _BITS16, dev)
+    if prefix.k_code.device != dev:
+        raise ValueError(f"prefix: on {prefix.k_code.device}, the cache on {dev}")
+    for name, t, n in (("prefix_lens", prefix_lens, prefix.B), ("lens", lens, cache.B)):
+        if t is not None:
+            _need(name, t, (n,), (torch.int32,), dev)
+    max_prefix_len = prefix.capacity if max_prefix_len is None else int(max_prefix_len)
+    max_len = cache.capacity if max_len is None else int(max_len)
+    with torch.cuda.device(dev):
+        need = kv2_attention_shared_workspace_size(prefix, cache, H_q, max_prefix_len, max_len) if ws is None else 0
+        out, ws = _rows_call(Q, Q.shape, out_dtype, out, ws, need)
+        p, d = prefix.desc(), cache.desc()
+        _check(_get_lib().kv2_attention_shared(ctypes.byref(p), _ptr(prefix_lens), max_prefix_len, ctypes.byref(d),
+                                               _ptr(lens), max_len, _ptr(Q), H_q, float(sm_scale), _ptr(out),
+                                               out_dtype, _ptr(ws), ws.numel(), _stream(stream)))
     return out
 
 

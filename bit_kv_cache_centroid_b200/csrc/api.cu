@@ -349,6 +349,114 @@ kv2_status kv2_attention_chunk(const kv2_cache* c, int len, const uint16_t* Q, i
 
 namespace {
 
+// what the row attention kernel takes of a cache and its lengths
+kv2_status check_rows_cache(const char* what, const kv2_cache* c, const int32_t* lens, int max_len, int H_q) {
+  if (kv2_status st = check_cache(c, true, false); st != KV2_OK) return st;
+  if (c->r != 0 && c->r != 8 && c->r != 16) return fail(KV2_ERR_UNSUPPORTED, "%s: r=%d (supported 0, 8, 16)", what, c->r);
+  if (H_q <= 0 || H_q % c->H_kv)
+    return fail(KV2_ERR_UNSUPPORTED, "%s: H_q=%d not a multiple of H_kv=%d", what, H_q, c->H_kv);
+  if (max_len < 0 || max_len > c->capacity)
+    return fail(KV2_ERR_CAPACITY, "%s: max_len=%d outside 0..capacity=%d", what, max_len, c->capacity);
+  if (reinterpret_cast<uintptr_t>(lens) & 3u) return fail(KV2_ERR_INVALID_ARG, "%s: lengths not 4-byte aligned", what);
+  return KV2_OK;
+}
+
+kv2_status check_rows_io(const char* what, const uint16_t* Q, const void* out, int out_dtype, const void* ws,
+                         size_t ws_bytes, size_t need) {
+  if (out_dtype != KV2_OUT_F32 && out_dtype != KV2_OUT_BF16)
+    return fail(KV2_ERR_INVALID_ARG, "%s: out_dtype=%d", what, out_dtype);
+  if (!Q || !out || !aligned16(Q) || !aligned16(out))
+    return fail(KV2_ERR_INVALID_ARG, "%s: Q / out NULL or not 16-byte aligned", what);
+  if (!ws || !aligned16(ws)) return fail(KV2_ERR_INVALID_ARG, "%s: ws NULL or not 16-byte aligned", what);
+  if (ws_bytes < need) return fail(KV2_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", what, ws_bytes, need);
+  return KV2_OK;
+}
+
+// rows per KV head and sequence, and row blocks over the heads, are ints in the kernel
+bool rows_too_many(const kv2_cache* c, int H_q, long long Nq) {
+  return Nq * (H_q / c->H_kv) > (1ll << 30) || Nq * H_q > (1ll << 30);
+}
+
+kv2::RowsArgs cross_args(const kv2_cache* c, const int32_t* lens, int max_len, const int32_t* q_lens, int Nq, int H_q) {
+  kv2::RowsArgs a{};
+  a.src[0] = {c, lens, q_lens, max_len, Nq};
+  a.nsrc = 1;
+  a.H_q = H_q;
+  return a;
+}
+kv2::RowsArgs shared_args(const kv2_cache* pre, const int32_t* prefix_lens, int max_prefix_len, const kv2_cache* c,
+                          const int32_t* lens, int max_len, int H_q) {
+  kv2::RowsArgs a{};
+  a.src[0] = {pre, prefix_lens, nullptr, max_prefix_len, c->B / pre->B};
+  a.src[1] = {c, lens, nullptr, max_len, 1};
+  a.nsrc = 2;
+  a.H_q = H_q;
+  return a;
+}
+
+}  // namespace
+
+size_t kv2_attention_cross_workspace_size(const kv2_cache* c, int H_q, int Nq, int max_len) {
+  if (!c || H_q <= 0 || c->H_kv <= 0 || H_q % c->H_kv || Nq < 0 || max_len < 0) return 0;
+  if (check_cache(c, false, false) != KV2_OK || rows_too_many(c, H_q, Nq)) return 0;
+  return kv2::rows_workspace_bytes(cross_args(c, nullptr, max_len, nullptr, Nq, H_q));
+}
+
+kv2_status kv2_attention_cross(const kv2_cache* c, const int32_t* lens, int max_len, const uint16_t* Q,
+                               const int32_t* q_lens, int Nq, int H_q, float sm_scale, void* out, int out_dtype,
+                               void* ws, size_t ws_bytes, void* stream) {
+  const CallRange range_("kv2_attention_cross");
+  kv2_status st = check_rows_cache("cross", c, lens, max_len, H_q);
+  if (st != KV2_OK) return st;
+  if (reinterpret_cast<uintptr_t>(q_lens) & 3u) return fail(KV2_ERR_INVALID_ARG, "cross: q_lens not 4-byte aligned");
+  if (Nq < 0) return fail(KV2_ERR_INVALID_ARG, "cross: Nq=%d", Nq);
+  if (rows_too_many(c, H_q, Nq)) return fail(KV2_ERR_UNSUPPORTED, "cross: Nq=%d x H_q=%d above 2^30", Nq, H_q);
+  if (Nq == 0) return ok();
+  kv2::RowsArgs a = cross_args(c, lens, max_len, q_lens, Nq, H_q);
+  st = check_rows_io("cross", Q, out, out_dtype, ws, ws_bytes, kv2::rows_workspace_bytes(a));
+  if (st != KV2_OK) return st;
+  a.Q = Q;
+  a.sm_scale = sm_scale;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.ws = ws;
+  return cuda_status(kv2::launch_rows(a, static_cast<cudaStream_t>(stream)), "cross launch");
+}
+
+size_t kv2_attention_shared_workspace_size(const kv2_cache* pre, const kv2_cache* c, int H_q, int max_prefix_len,
+                                           int max_len) {
+  if (!pre || !c || H_q <= 0 || c->H_kv <= 0 || H_q % c->H_kv || max_prefix_len < 0 || max_len < 0) return 0;
+  if (check_cache(pre, false, false) != KV2_OK || check_cache(c, false, false) != KV2_OK) return 0;
+  if (pre->H_kv != c->H_kv || pre->d != c->d || c->B % pre->B || rows_too_many(c, H_q, c->B)) return 0;
+  return kv2::rows_workspace_bytes(shared_args(pre, nullptr, max_prefix_len, c, nullptr, max_len, H_q));
+}
+
+kv2_status kv2_attention_shared(const kv2_cache* pre, const int32_t* prefix_lens, int max_prefix_len,
+                                const kv2_cache* c, const int32_t* lens, int max_len, const uint16_t* Q, int H_q,
+                                float sm_scale, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  const CallRange range_("kv2_attention_shared");
+  kv2_status st = check_rows_cache("shared prefix", pre, prefix_lens, max_prefix_len, H_q);
+  if (st != KV2_OK) return st;
+  st = check_rows_cache("shared", c, lens, max_len, H_q);
+  if (st != KV2_OK) return st;
+  if (pre->H_kv != c->H_kv || pre->d != c->d)
+    return fail(KV2_ERR_INVALID_ARG, "shared: prefix has %d heads of %d channels, the cache %d of %d", pre->H_kv, pre->d,
+                c->H_kv, c->d);
+  if (c->B % pre->B) return fail(KV2_ERR_INVALID_ARG, "shared: %d sequences for %d prefixes", c->B, pre->B);
+  if (rows_too_many(c, H_q, c->B)) return fail(KV2_ERR_UNSUPPORTED, "shared: B=%d x H_q=%d above 2^30", c->B, H_q);
+  kv2::RowsArgs a = shared_args(pre, prefix_lens, max_prefix_len, c, lens, max_len, H_q);
+  st = check_rows_io("shared", Q, out, out_dtype, ws, ws_bytes, kv2::rows_workspace_bytes(a));
+  if (st != KV2_OK) return st;
+  a.Q = Q;
+  a.sm_scale = sm_scale;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.ws = ws;
+  return cuda_status(kv2::launch_rows(a, static_cast<cudaStream_t>(stream)), "shared launch");
+}
+
+namespace {
+
 // one stream of a paged cache: device base and bytes per token slot
 struct PageStream {
   char* base;

@@ -125,6 +125,26 @@ struct ChunkArgs {
 size_t chunk_workspace_bytes(const kv2_cache& c, int H_q, int Nq);
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t s);
 
+// Rows of queries that read the same keys (tcgen05): one source (cross
+// attention) or two (a shared prefix, then each sequence's own cache).
+struct RowsInput {
+  const kv2_cache* c;
+  const int32_t* lens;    // device [B]: cached tokens per sequence (null: max_len each)
+  const int32_t* q_lens;  // device [B]: queries per sequence (null: Nq each)
+  int max_len, Nq;
+};
+struct RowsArgs {
+  RowsInput src[2];
+  int nsrc, H_q;
+  const uint16_t* Q;      // bf16 [src[0].B][src[0].Nq][H_q][d]; the same rows for both sources
+  float sm_scale;
+  void* out;
+  int out_dtype;
+  void* ws;
+};
+size_t rows_workspace_bytes(const RowsArgs& a);
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s);
+
 // Records the detail returned by kv2_last_error() on this thread; returns st.
 kv2_status set_last_error(kv2_status st, const char* fmt, ...);
 // Every check kv2_attention_decode makes except those of the workspace; on

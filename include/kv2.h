@@ -373,6 +373,82 @@ kv2_status kv2_attention_chunk(const kv2_cache* cache, int len, const uint16_t* 
                                void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Workspace for kv2_attention_cross, in bytes: a 256-byte header whose first
+ * 32-bit word is the sticky error word, the tile list's bookkeeping (8 bytes
+ * per sequence, 16 per CTA), and for each CTA two pieces of cut units (per
+ * query row d sums, the running maximum and the softmax denominator, fp32; 16
+ * to 128 rows). At most about 20 MB. Returns 0 for unsupported shapes.
+ */
+size_t kv2_attention_cross_workspace_size(const kv2_cache* cache, int H_q, int Nq, int max_len);
+
+/*
+ * kv2_attention_cross — Nq queries per sequence against the first lens[b]
+ * cached tokens of sequence b, every one visible to every query (no mask
+ * between them): cross attention to states of another length, such as an
+ * encoder's, kept in the packed cache. Nq = 1 is its decode form. The score is
+ * the compensated one of "2. PSAC" in the QuantWM article, q.(k^ + P a) =
+ * q.k^ + (qP).a, over the 2-bit cache unpacked inside the kernel; softmax over
+ * the sequence's tokens; values dequantized inside the kernel. The pages have
+ * no counterpart for the lengths.
+ * lens   : int32 [B] (device), tokens of each sequence; values are taken into
+ *          0..max_len; NULL: max_len each. A sequence of no tokens gives zeros.
+ * q_lens : int32 [B] (device), queries of each sequence, taken into 0..Nq;
+ *          NULL: Nq each. Rows of out at or after q_lens[b] are not written.
+ * max_len: 0..capacity; sizes the launch and the workspace. The work follows
+ *          the lengths on the device, so a captured call may be replayed with
+ *          other lengths.
+ * Q      : bf16 [B][Nq][H_q][d]; out: [B][Nq][H_q][d], fp32 or bf16.
+ * Requires r in {0, 8, 16}; any H_q / H_kv; contiguous or paged cache (block
+ * table entries of pages below the length must be valid).
+ * Arithmetic: as kv2_attention_chunk (tcgen05, fp16 operands, fp32 sums):
+ * keys fp16(code*s + fp16(z + centroid)), values fp16(code*s + z), queries
+ * scaled per row by a power of two (exact), (qP) rounded to fp16,
+ * probabilities fp16 against a running maximum that may trail the true one by
+ * a factor of 2^7.
+ * ws     : device workspace of kv2_attention_cross_workspace_size bytes, its
+ *          first 32-bit word zeroed by the caller before the first use: the
+ *          kernel sets it to 1 when one of its waits runs out of its budget
+ *          (KV2_WAIT_BUDGET_CYCLES); rows it had not finished are then NaN.
+ *          Calls that share a workspace must not overlap.
+ */
+kv2_status kv2_attention_cross(const kv2_cache* cache, const int32_t* lens, int max_len, const uint16_t* Q,
+                               const int32_t* q_lens, int Nq, int H_q, float sm_scale, void* out, int out_dtype,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Workspace for kv2_attention_shared, in bytes: as
+ * kv2_attention_cross_workspace_size, plus every row's result over the prefix
+ * and over its own cache (2 * B * H_q * (d + 2) fp32). Returns 0 for
+ * unsupported shapes.
+ */
+size_t kv2_attention_shared_workspace_size(const kv2_cache* prefix, const kv2_cache* cache, int H_q,
+                                           int max_prefix_len, int max_len);
+
+/*
+ * kv2_attention_shared — one decode query per sequence, where groups of
+ * sequences share a prefix that is stored and read once for all of them. The
+ * cache->B sequences form prefix->B equal groups of consecutive sequences;
+ * sequence b attends to the first prefix_lens[b / (cache->B / prefix->B)]
+ * tokens of its group's prefix and to the first lens[b] tokens of its own
+ * cache. The result is that of kv2_attention_decode's formula over both
+ * together; tokens and heads not within a length take no part.
+ * prefix, cache: the same H_kv and d; all else (M, r, group, coefficient
+ *          format, contiguous or paged) may differ. The two may be views of
+ *          one pool of pages through two block tables.
+ * prefix_lens  : int32 [prefix->B], lens: int32 [cache->B] (device), taken
+ *          into 0..max_prefix_len and 0..max_len; NULL: the maximum each. A
+ *          query with no token at all gives zeros.
+ * Q, out : bf16 [B][H_q][d]; fp32 or bf16 [B][H_q][d].
+ * Requirements, arithmetic, replay and ws: as kv2_attention_cross.
+ * Errors: KV2_ERR_INVALID_ARG (cache->B not a multiple of prefix->B, different
+ * H_kv or d, NULL or misaligned pointers), KV2_ERR_UNSUPPORTED (r),
+ * KV2_ERR_CAPACITY (a maximum beyond its cache), KV2_ERR_WORKSPACE.
+ */
+kv2_status kv2_attention_shared(const kv2_cache* prefix, const int32_t* prefix_lens, int max_prefix_len,
+                                const kv2_cache* cache, const int32_t* lens, int max_len, const uint16_t* Q, int H_q,
+                                float sm_scale, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Pages of a paged cache moved out of HBM and back (long-horizon memory:
  * a sequence's older chunks kept in host memory and brought back when the
  * caller wants them in the attention window again; which pages to move is
