@@ -6,7 +6,8 @@ for device memory and streams only. If ``libkv2.so`` is missing or fails to
 load, importing the binding raises: there is no CPU fallback.
 
 Names follow the C ABI: ``kv2_fit_psac_basis``, ``kv2_fit_centroids``, ``kv2_quantize_append``,
-``kv2_attention_decode``, ``kv2_attention_chunk`` and the workspace-size
+``kv2_rotary_append``, ``kv2_attention_decode``, ``kv2_attention_chunk``,
+``kv2_attention_cross``, ``kv2_attention_shared`` and the workspace-size
 queries. ``Cache`` owns the device buffers of one packed cache and builds the
 ``kv2_cache`` descriptor.
 """
@@ -46,6 +47,11 @@ class kv2_cache(ctypes.Structure):
                 ("psac_fmt", ctypes.c_int32), ("psac_scale", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("page_tokens", ctypes.c_int32),
                 ("group", ctypes.c_int32)]
+
+
+class kv2_rotary(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 def _load():
@@ -98,6 +104,10 @@ def _load():
     L.kv2_attention_shared_workspace_size.argtypes = [C, C, I, I, I]
     L.kv2_attention_shared.restype = I
     L.kv2_attention_shared.argtypes = [C, P, I, C, P, I, P, I, F, P, I, P, S, P]
+    L.kv2_rotary_append_workspace_size.restype = S
+    L.kv2_rotary_append_workspace_size.argtypes = [C, I]
+    L.kv2_rotary_append.restype = I
+    L.kv2_rotary_append.argtypes = [C, ctypes.POINTER(kv2_rotary), P, P, P, P, I, P, P, P, I, I, P, S, P]
     L.kv2_page_bytes.restype = S
     L.kv2_page_bytes.argtypes = [ctypes.POINTER(kv2_cache)]
     L.kv2_page_store.restype = I
@@ -128,7 +138,8 @@ def __getattr__(name):
 EXPORTS = ["kv2_status_string", "kv2_last_error", "kv2_version", "kv2_fit_workspace_size",
            "kv2_fit_psac_basis", "kv2_fit_centroids_workspace_size", "kv2_fit_centroids",
            "kv2_top1_workspace_size", "kv2_decode_top1", "kv2_dense_top1",
-           "kv2_quantize_append", "kv2_decode_workspace_size",
+           "kv2_quantize_append", "kv2_rotary_append_workspace_size", "kv2_rotary_append",
+           "kv2_decode_workspace_size",
            "kv2_attention_decode", "kv2_attention_decode_noalloc", "kv2_decode_noalloc_error",
            "kv2_append_attention_decode",
            "kv2_chunk_workspace_size", "kv2_attention_chunk",
@@ -409,7 +420,7 @@ def kv2_attention_chunk(cache: Cache, length: int, Q: torch.Tensor, Kself: torch
 
 
 # ----------------------------------------------------------------------------
-# rows of queries: cross attention, decode over a shared prefix
+# appends with the position rotation applied on the way
 # ----------------------------------------------------------------------------
 
 def _need(name, t, shape, dtypes, device):
@@ -426,6 +437,70 @@ def _need(name, t, shape, dtypes, device):
 
 _BITS16 = (torch.bfloat16, torch.int16)
 
+
+class Rotary:
+    """Position rotation of keys and queries: cos_sin fp32 [positions][rot] on
+    the device, rot/2 cosines then rot/2 sines per row; channel i pairs with
+    i + rot/2, or with ``interleaved`` channels 2i and 2i + 1."""
+
+    def __init__(self, cos_sin: torch.Tensor, interleaved: bool = False):
+        if cos_sin.dim() != 2:
+            raise ValueError(f"cos_sin: {cos_sin.dim()} dimensions, expected [positions][rot]")
+        _need("cos_sin", cos_sin, cos_sin.shape, (torch.float32,), cos_sin.device)
+        self.cos_sin, self.interleaved = cos_sin, bool(interleaved)
+
+    def desc(self) -> kv2_rotary:
+        return kv2_rotary(self.cos_sin.data_ptr(), self.cos_sin.shape[0], self.cos_sin.shape[1], int(self.interleaved))
+
+
+def kv2_rotary_append_workspace_size(cache: Cache, n_new: int) -> int:
+    d = cache.desc()
+    return int(_get_lib().kv2_rotary_append_workspace_size(ctypes.byref(d), n_new))
+
+
+def kv2_rotary_append(cache: Cache, rotary: Rotary, K: torch.Tensor, V: torch.Tensor, positions: torch.Tensor,
+                      start: torch.Tensor, candidates: int, count=None, Q=None, Q_out=None, ws=None, stream=None):
+    """Rotate keys (and queries) by their positions and append keys and values:
+    K, V bf16 [B][n_new][H_kv][d]; positions int32 [B][n_new] rows of the
+    rotation's table; token i of sequence b goes to slot start[b] + i, for i <
+    count[b] (None: all). Q bf16 [B][n_new][H_q][d] -> Q_out (made when not
+    passed; may be Q), returned; without Q, None."""
+    if K.dim() != 4:
+        raise ValueError(f"K: {K.dim()} dimensions, expected [B][n_new][H_kv][d]")
+    n_new, dev = K.shape[1], cache.k_code.device
+    for name, t in (("K", K), ("V", V)):
+        _need(name, t, (cache.B, n_new, cache.H_kv, cache.d), _BITS16, dev)
+    _need("positions", positions, (cache.B, n_new), (torch.int32,), dev)
+    for name, t in (("start", start), ("count", count)):
+        if t is not None or name == "start":
+            _need(name, t, (cache.B,), (torch.int32,), dev)
+    if rotary.cos_sin.device != dev:
+        raise ValueError(f"cos_sin: on {rotary.cos_sin.device}, expected {dev}")
+    H_q = 0
+    if Q is not None:
+        if Q.dim() != 4:
+            raise ValueError(f"Q: {Q.dim()} dimensions, expected [B][n_new][H_q][d]")
+        H_q = Q.shape[2]
+        _need("Q", Q, (cache.B, n_new, H_q, cache.d), _BITS16, dev)
+    elif Q_out is not None:
+        raise ValueError("Q_out without Q")
+    with torch.cuda.device(dev):
+        if Q is not None:
+            Q_out = torch.zeros_like(Q) if Q_out is None else Q_out
+            _need("Q_out", Q_out, Q.shape, _BITS16, dev)
+        if ws is None:
+            # zeroed: the first word is the sticky error word
+            ws = torch.zeros(max(kv2_rotary_append_workspace_size(cache, n_new), 16), dtype=torch.uint8, device=dev)
+        d, r = cache.desc(), rotary.desc()
+        _check(_get_lib().kv2_rotary_append(ctypes.byref(d), ctypes.byref(r), _ptr(K), _ptr(V), _ptr(Q), _ptr(Q_out), H_q,
+                                            _ptr(positions), _ptr(start), _ptr(count), n_new, candidates, _ptr(ws),
+                                            ws.numel(), _stream(stream)))
+    return Q_out
+
+
+# ----------------------------------------------------------------------------
+# rows of queries: cross attention, decode over a shared prefix
+# ----------------------------------------------------------------------------
 
 def _rows_call(Q, shape, out_dtype, out, ws, need):
     """Output and workspace of a row attention call (made when not passed)."""

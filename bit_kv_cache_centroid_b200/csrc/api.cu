@@ -225,6 +225,12 @@ kv2::QuantizeArgs quantize_args(const kv2_cache* c, const uint16_t* K, const uin
   return a;
 }
 
+// rows of a rotary append are ints in the kernels
+bool rotary_too_many(const kv2_cache* c, int n_new, int H_q) {
+  const long long rows = static_cast<long long>(c->B) * n_new;
+  return rows > (1ll << 30) || rows * c->H_kv > (1ll << 30) || rows * H_q > (1ll << 40);
+}
+
 // argument checks of a decode call (the cache already checked)
 // Decode arguments other than the workspace.
 kv2_status check_decode_args(const kv2_cache* c, int len, const uint16_t* Q, int H_q, void* out, int out_dtype) {
@@ -273,6 +279,49 @@ kv2_status kv2_quantize_append(const kv2_cache* c, const uint16_t* K, const uint
   if (n_new == 0) return ok();
   return cuda_status(kv2::launch_quantize(quantize_args(c, K, V, n_new, pos, candidates),
                                           static_cast<cudaStream_t>(stream)), "quantize launch");
+}
+
+size_t kv2_rotary_append_workspace_size(const kv2_cache* c, int n_new) {
+  if (!c || n_new < 0 || check_cache(c, false, false) != KV2_OK || rotary_too_many(c, n_new, 1)) return 0;
+  return kv2::rotary_workspace_bytes(*c, n_new);
+}
+
+kv2_status kv2_rotary_append(const kv2_cache* c, const kv2_rotary* rot, const uint16_t* K, const uint16_t* V,
+                             const uint16_t* Q, uint16_t* Q_out, int H_q, const int32_t* positions,
+                             const int32_t* start, const int32_t* count, int n_new, int candidates, void* ws,
+                             size_t ws_bytes, void* stream) {
+  const CallRange range_("kv2_rotary_append");
+  kv2_status st = check_cache(c, true, true);
+  if (st != KV2_OK) return st;
+  if (!rot) return fail(KV2_ERR_INVALID_ARG, "rotary: descriptor is NULL");
+  if (rot->rot < 2 || rot->rot > c->d || (rot->rot & 1))
+    return fail(KV2_ERR_UNSUPPORTED, "rotary: rot=%d (even, 2..d=%d)", rot->rot, c->d);
+  if (rot->positions < 0 || (rot->interleaved != 0 && rot->interleaved != 1))
+    return fail(KV2_ERR_INVALID_ARG, "rotary: positions=%d interleaved=%d", rot->positions, rot->interleaved);
+  if (n_new < 0) return fail(KV2_ERR_INVALID_ARG, "rotary: n_new=%d < 0", n_new);
+  if (candidates < 1 || candidates > c->M)
+    return fail(KV2_ERR_INVALID_ARG, "rotary: candidates=%d outside 1..M=%d", candidates, c->M);
+  if (Q && H_q <= 0) return fail(KV2_ERR_INVALID_ARG, "rotary: H_q=%d", H_q);
+  if (rotary_too_many(c, n_new, Q ? H_q : 1))
+    return fail(KV2_ERR_UNSUPPORTED, "rotary: B=%d x n_new=%d tokens above 2^30 rows", c->B, n_new);
+  if (n_new == 0) return ok();
+  if (!rot->cos_sin || !aligned16(rot->cos_sin))
+    return fail(KV2_ERR_INVALID_ARG, "rotary: cos_sin NULL or not 16-byte aligned");
+  if (!K || !V || !aligned16(K) || !aligned16(V))
+    return fail(KV2_ERR_INVALID_ARG, "rotary: K / V NULL or not 16-byte aligned");
+  if (Q && (!Q_out || !aligned16(Q) || !aligned16(Q_out)))
+    return fail(KV2_ERR_INVALID_ARG, "rotary: Q_out NULL, or Q / Q_out not 16-byte aligned");
+  const uintptr_t ints = reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(start) |
+                         reinterpret_cast<uintptr_t>(count);
+  if (!positions || !start || (ints & 3u))
+    return fail(KV2_ERR_INVALID_ARG, "rotary: positions / start NULL, or not 4-byte aligned");
+  if (!ws || !aligned16(ws)) return fail(KV2_ERR_INVALID_ARG, "rotary: ws NULL or not 16-byte aligned");
+  const size_t need = kv2::rotary_workspace_bytes(*c, n_new);
+  if (ws_bytes < need) return fail(KV2_ERR_WORKSPACE, "rotary: workspace %zu < %zu bytes", ws_bytes, need);
+  kv2::RotaryArgs a{c, rot->cos_sin, rot->positions, rot->rot, rot->interleaved, K, V, Q, Q_out, Q ? H_q : 0,
+                    positions, start, count, n_new, candidates, ws};
+  return cuda_status(kv2::launch_rotary(a, quantize_args(c, K, V, n_new, 0, candidates),
+                                        static_cast<cudaStream_t>(stream)), "rotary append launch");
 }
 
 size_t kv2_decode_workspace_size(const kv2_cache* c, int H_q, int len) {

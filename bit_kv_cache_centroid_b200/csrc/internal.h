@@ -45,8 +45,34 @@ struct QuantizeArgs {
   const int32_t* table = nullptr;
   int page = 0;
   int group = kGroup;  // channels per (scale, zero) group: 32, 64 or 128
+  // rows with places of their own, written by the kernel just before on the
+  // stream (the key kernel is then its programmatic dependent): row i of K
+  // [*n_rows][H][d] goes to offset rows[i].y of sequence or page rows[i].x
+  // (negative: not stored); B * n_new bounds their number; V null: values are
+  // coded elsewhere
+  const int2* rows = nullptr;
+  const int* n_rows = nullptr;
 };
 cudaError_t launch_quantize(const QuantizeArgs& a, cudaStream_t s);
+
+// Append with the position rotation applied on the way, at per-sequence places.
+struct RotaryArgs {
+  const kv2_cache* c;
+  const float* cos_sin;      // [positions][rot]: rot/2 cosines, rot/2 sines
+  int positions, rot, interleaved;
+  const uint16_t* K;         // bf16 [B][n_new][H_kv][d]
+  const uint16_t* V;
+  const uint16_t* Q;         // bf16 [B][n_new][H_q][d] (null: no queries)
+  uint16_t* Q_out;
+  int H_q;
+  const int32_t* position;   // [B][n_new]
+  const int32_t* start;      // [B]
+  const int32_t* count;      // [B] (null: n_new each)
+  int n_new, candidates;
+  void* ws;
+};
+size_t rotary_workspace_bytes(const kv2_cache& c, int n_new);
+cudaError_t launch_rotary(const RotaryArgs& a, const QuantizeArgs& q, cudaStream_t s);
 
 // QSAC-aware centre fitting (Lloyd iterations with the QSAC assignment).
 struct FitCentroidsArgs {

@@ -72,6 +72,7 @@
 // with one key (short appends) runs the products as fp32 FMAs (e_dot = 0).
 #include <cfloat>
 
+#include "codec.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -221,44 +222,14 @@ __device__ __forceinline__ void perturbation2(const uint16_t* rows, const int (&
   }
 }
 
-// Codes of the 32 values x of one sub-group with the group's (s, z): the
-// quotient (x - z) * inv_s rounded to the nearest integer and clamped to
-// 0..3, two channels per packed instruction (each lane rounded as its scalar
-// form); bit c of `redo` flags a quotient within 2^-18 of a half-integer
-// (|q - rint(q)| > 1/2 - 2^-18), whose code the correctly rounded division
-// must decide. With E, also the residual errors x - (code * s + z). A group
-// of scale 0 holds x = z only (z is the rounded-down minimum and s the
-// rounded-up range / 3): its codes are 0 and its errors x - z whatever the
-// quotient gave.
-template <bool E>
-__device__ __forceinline__ void code32(const float (&x)[kGroup], const GroupParams& gp, float inv_s,
-                                       uint32_t& w0, uint32_t& w1, uint32_t& redo, float (&ev)[kGroup]) {
-  const f32x2 z2 = pk2(gp.z, gp.z), is2 = pk2(inv_s, inv_s), s2 = pk2(gp.s, gp.s);
-  w0 = w1 = redo = 0;
-#pragma unroll
-  for (int c = 0; c < kGroup; c += 2) {
-    const float2 qa = up2(fmul2(fsub2(pk2(x[c], x[c + 1]), z2), is2));
-    const float r0 = rintf(qa.x), r1 = rintf(qa.y);
-    redo |= (uint32_t(fabsf(__fsub_rn(qa.x, r0)) > 0.5f - 0x1p-18f) << c) |
-            (uint32_t(fabsf(__fsub_rn(qa.y, r1)) > 0.5f - 0x1p-18f) << (c + 1));
-    const float c0 = fminf(fmaxf(r0, 0.0f), 3.0f), c1 = fminf(fmaxf(r1, 0.0f), 3.0f);
-    const uint32_t q = uint32_t(c0) | (uint32_t(c1) << 2);
-    if (c < 16) w0 |= q << (2 * c); else w1 |= q << (2 * (c - 16));
-    if constexpr (E) {
-      const float2 e = up2(fsub2(pk2(x[c], x[c + 1]), ffma2(pk2(c0, c1), s2, z2)));
-      ev[c] = e.x;
-      ev[c + 1] = e.y;
-    }
-  }
-  if (gp.s == 0.0f) w0 = w1 = redo = 0;
-}
-
 // warp-wide minimum of 64-bit keys (every lane gets it)
 __device__ __forceinline__ unsigned long long warp_min64(unsigned long long v) {
   const uint32_t hi = __reduce_min_sync(0xffffffffu, uint32_t(v >> 32));
   const uint32_t lo = __reduce_min_sync(0xffffffffu, uint32_t(v >> 32) == hi ? uint32_t(v) : 0xFFFFFFFFu);
   return (static_cast<unsigned long long>(hi) << 32) | lo;
 }
+
+constexpr size_t kNoSlot = ~size_t(0);   // a row that is not stored
 
 constexpr int kListLen = 15;   // listed centres per key in the decision by perturbations (slot 15: count and limit)
 
@@ -342,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, CPL >= 16 ? 1 : 2) quantize_kernel(Q
   // work: the tiles of every head in one list (head-major); CTA b takes the
   // b-th of gridDim.x equal runs, so every resident CTA has the same number
   // of tiles, and stages a head's tables when its run enters that head
-  const int rows_total = a.B * a.n_new;
+  if (a.rows) asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel that writes rows and keys
+  const int rows_total = a.rows ? *a.n_rows : a.B * a.n_new;
   const int ntiles = (rows_total + KT - 1) / KT;       // per head
   const long long nwork = static_cast<long long>(ntiles) * a.H;
   const long long lo = nwork * blockIdx.x / gridDim.x, hi = nwork * (blockIdx.x + 1) / gridDim.x;
@@ -356,6 +328,10 @@ __global__ void __launch_bounds__(kThreads, CPL >= 16 ? 1 : 2) quantize_kernel(Q
     return base + ((size_t(b) * a.n_new + t) * a.H + h) * D;
   };
   auto slot_of = [&](int row) {
+    if (a.rows) {
+      const int2 at = a.rows[row];
+      return at.x < 0 ? kNoSlot : (size_t(at.x) * a.H + h) * size_t(a.table ? a.page : a.cap) + at.y;
+    }
     const int b = row / a.n_new, t = row - b * a.n_new;
     return cache_slot(a.table, a.page, a.H, a.cap, b, h, a.pos + t);
   };
@@ -779,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, CPL >= 16 ? 1 : 2) quantize_kernel(Q
 #pragma unroll
       for (int k = 0; k < NS; ++k) {
         kx[k] = __uint_as_float(uint32_t(krow[k * kGroup + lane]) << 16);
-        vx[k] = a.assign ? 0.0f : __uint_as_float(uint32_t(vrow[k * kGroup + lane]) << 16);
+        vx[k] = a.assign || !a.V ? 0.0f : __uint_as_float(uint32_t(vrow[k * kGroup + lane]) << 16);
       }
       // ---- perturbation estimate: lane (candidate i, group g) takes the
       // group's scale; E_i = fmaf chain over ascending g of (W_g s_g) s_g;
@@ -829,13 +805,14 @@ __global__ void __launch_bounds__(kThreads, CPL >= 16 ? 1 : 2) quantize_kernel(Q
       }
       if (a.assign) {
         if (lane == 0) a.assign[size_t(row) * a.H + h] = jc;
-      } else {
+      } else if (slot_of(row) != kNoSlot) {
       // ---- K residual and V codecs, lane = channel of each 32-channel
       // sub-group; a group's range spans its SPG sub-groups and the lanes
       const __half* crow = cent + size_t(jc) * D;      // lanes read consecutive channels
       const size_t slot = slot_of(row);
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
+        if (which == 1 && !a.V) break;                 // values coded elsewhere
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float x[SPG];
@@ -1056,8 +1033,8 @@ __global__ void __launch_bounds__(kThreads, CPL >= 16 ? 1 : 2) quantize_kernel(Q
 #pragma unroll
           for (int cc = 0; cc < kGroup; ++cc) ev[t][cc] = cc == c ? e : ev[t][cc];
         }
-        if (live) {
-          const size_t slot = slot_of(row_of(k));
+        const size_t slot = live ? slot_of(row_of(k)) : kNoSlot;
+        if (slot != kNoSlot) {
           *reinterpret_cast<uint2*>(a.k_code + slot * (D / 16) + sg * 2) = make_uint2(w0, w1);
           if (sg % SPG == 0) a.k_sz[slot * NG + sg / SPG] = uint32_t(gp.s_bits) | (uint32_t(gp.z_bits) << 16);
           if (sg == 0) {
@@ -1087,14 +1064,18 @@ __global__ void __launch_bounds__(kThreads, CPL >= 16 ? 1 : 2) quantize_kernel(Q
       float acc = 0.0f;
 #pragma unroll 8
       for (int c = 0; c < D; ++c) acc = __fmaf_rn(Pcol[c * a.r], e[c + (c >> 5)], acc);
-      if (r8) psa_w[k * a.r + i] = acc;
-      else a.psac[slot_of(row_of(k)) * a.r + i] = f16_rn(acc);
+      if (r8) {
+        psa_w[k * a.r + i] = acc;
+      } else {
+        const size_t slot = slot_of(row_of(k));
+        if (slot != kNoSlot) a.psac[slot * a.r + i] = f16_rn(acc);
+      }
     }
     if (r8) {
       __syncwarp();
       for (int k = lane; k < nk; k += 32) {
         const size_t slot = slot_of(row_of(k));
-        psac_int8(psa_w + k * a.r, a.r, reinterpret_cast<int8_t*>(a.psac) + slot * a.r, a.psac_scale + slot);
+        if (slot != kNoSlot) psac_int8(psa_w + k * a.r, a.r, reinterpret_cast<int8_t*>(a.psac) + slot * a.r, a.psac_scale + slot);
       }
     }
     }
@@ -1124,40 +1105,8 @@ __global__ void __launch_bounds__(256) value_codec_kernel(QuantizeArgs a) {
   const long long row = rh / a.H;
   const int b = int(row / a.n_new), tok = int(row % a.n_new);
   const uint16_t* vrow = a.V + ((size_t(b) * a.n_new + tok) * a.H + h) * D + sg * kGroup;
-  float x[kGroup];
-#pragma unroll
-  for (int c8 = 0; c8 < kGroup / 8; ++c8) {
-    const uint4 vv = *reinterpret_cast<const uint4*>(vrow + c8 * 8);
-    const uint32_t vu[4] = {vv.x, vv.y, vv.z, vv.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      x[c8 * 8 + 2 * q] = __uint_as_float(vu[q] << 16);
-      x[c8 * 8 + 2 * q + 1] = __uint_as_float(vu[q] & 0xffff0000u);
-    }
-  }
-  float mn = x[0], mx = x[0];
-#pragma unroll
-  for (int c = 1; c + 1 < kGroup; c += 2) { mn = fmin3(mn, x[c], x[c + 1]); mx = fmax3(mx, x[c], x[c + 1]); }
-  mn = fminf(mn, x[kGroup - 1]);
-  mx = fmaxf(mx, x[kGroup - 1]);
-#pragma unroll
-  for (int o = 1; o < SPG; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  }
-  const GroupParams gp = group_params(mn, mx);
-  const float inv_s = __frcp_rn(gp.s);
-  uint32_t w0, w1, redo;
-  float unused[kGroup];
-  code32<false>(x, gp, inv_s, w0, w1, redo, unused);
-  // the rare channels whose code the correctly rounded division decides
-#pragma unroll 1
-  for (; redo; redo &= redo - 1) {
-    const int c = __ffs(redo) - 1;
-    const uint32_t q = group_code(__uint_as_float(uint32_t(vrow[c]) << 16), gp);
-    if (c < 16) w0 = (w0 & ~(3u << (2 * c))) | (q << (2 * c));
-    else w1 = (w1 & ~(3u << (2 * (c - 16)))) | (q << (2 * (c - 16)));
-  }
+  uint32_t w0, w1;
+  const GroupParams gp = code_values<GS>(vrow, w0, w1);
   if (live) {
     const size_t slot = cache_slot(a.table, a.page, a.H, a.cap, b, h, a.pos + tok);
     *reinterpret_cast<uint2*>(a.v_code + slot * (D / 16) + sg * 2) = make_uint2(w0, w1);
@@ -1188,7 +1137,22 @@ cudaError_t launch_cfg(const QuantizeArgs& a, cudaStream_t s) {
   const int rows = a.B * a.n_new;
   const long long nwork = static_cast<long long>((rows + Cfg::KT - 1) / Cfg::KT) * a.H;
   const long long resident = static_cast<long long>(sms) * per_sm;   // one wave of persistent CTAs
-  kern<<<unsigned(nwork < resident ? nwork : resident), kThreads, smem, s>>>(a);
+  const unsigned grid = unsigned(nwork < resident ? nwork : resident);
+  if (a.rows) {
+    // programmatic dependent of the kernel that writes its rows
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+  }
+  kern<<<grid, kThreads, smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || KPT == 1 || a.assign) return e;
   // the values of a multi-key append: the key kernel's programmatic dependent

@@ -238,6 +238,60 @@ kv2_status kv2_quantize_append(const kv2_cache* cache, const uint16_t* K, const 
                                int n_new, int pos, int candidates, void* stream);
 
 /*
+ * Position rotation (rotary embedding) of keys and queries. cos_sin: fp32
+ * [positions][rot] (device, 16-byte aligned); row p holds rot/2 cosines, then
+ * rot/2 sines of position p's angles. The first `rot` channels of a head turn
+ * (rot even, 2..d), the others stay. Pairs: channel i with i + rot/2
+ * (interleaved 0) or channels 2i, 2i + 1 (interleaved 1); pair i = (a, b)
+ * becomes (a cos_i - b sin_i, b cos_i + a sin_i). A table of any rows serves
+ * any scheme of positions (one row per token index, per latent grid point).
+ */
+typedef struct kv2_rotary {
+  const float* cos_sin;
+  int32_t positions, rot, interleaved;
+} kv2_rotary;
+
+/*
+ * Workspace for kv2_rotary_append, in bytes: a 256-byte header whose first
+ * 32-bit word is the sticky error word, 8 bytes per token, and the rotated
+ * keys (bf16). Returns 0 for unsupported shapes.
+ */
+size_t kv2_rotary_append_workspace_size(const kv2_cache* cache, int n_new);
+
+/*
+ * kv2_rotary_append — kv2_quantize_append at per-sequence places, with the
+ * position rotation applied to the keys (and queries) on the way.
+ * K, V     : bf16 [B][n_new][H_kv][d], a padded batch.
+ * Q, Q_out : bf16 [B][n_new][H_q][d]; Q NULL: keys and values only. Q_out may
+ *            be Q.
+ * positions: int32 [B][n_new] (device), the rotation table's row of each token.
+ * start    : int32 [B] (device): token i of sequence b goes to slot start[b] + i.
+ * count    : int32 [B] (device): tokens of each sequence, taken into
+ *            0..n_new; NULL: n_new each. Tokens behind the count are neither
+ *            read nor written, nor are their rows of Q_out.
+ * Keys and queries turn in fp32, every product and sum rounded to nearest,
+ * and are rounded once to bf16; the cache then holds, bit for bit, what
+ * kv2_quantize_append stores for those keys and values (PSAC coefficients: the
+ * same up to the order of their fp32 sums, which depends on the append's
+ * length). Lengths and places are read on the device, so a captured call may
+ * be replayed with others.
+ * A token whose slot lies outside 0..capacity-1, whose block-table entry is
+ * negative, or whose position lies outside the table is not stored, and the
+ * error word is set to 1 (the library never clears it; in the last case its
+ * rows of Q_out are NaN). Two tokens of one call on one slot race.
+ * ws       : device workspace of kv2_rotary_append_workspace_size bytes, its
+ *            first 32-bit word zeroed by the caller before the first use.
+ *            Calls that share a workspace must not overlap.
+ * Errors: those of kv2_quantize_append's cache and candidates;
+ * KV2_ERR_UNSUPPORTED (rot odd or outside 2..d, more than 2^30 rows),
+ * KV2_ERR_INVALID_ARG (NULL or misaligned pointers), KV2_ERR_WORKSPACE.
+ */
+kv2_status kv2_rotary_append(const kv2_cache* cache, const kv2_rotary* rotary, const uint16_t* K, const uint16_t* V,
+                             const uint16_t* Q, uint16_t* Q_out, int H_q, const int32_t* positions,
+                             const int32_t* start, const int32_t* count, int n_new, int candidates, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/*
  * Workspace for kv2_attention_decode, in bytes: a 256-byte header whose
  * first 32-bit word is the sticky error word (below), then the split-K
  * partials (per query head and split, d output sums, the running maximum and

@@ -116,3 +116,49 @@ def test_plain_attention_agrees_with_the_oracle(orc):
         for name, wrong in mistakes.items():
             with pytest.raises(AssertionError):
                 plain.check(wrong.float(), o, sigma, torch.float32, name)
+
+
+def rotary(lib, c, cs=0x100, positions=500, rot=128, inter=0, K=0x200, V=0x300, Q=0, Qo=0, H_q=4, pos=0x400, start=0x500,
+           count=0, n=3, C=4, ws=0x600, nb=1 << 30):
+    import bit_kv_cache_centroid_b200 as kv2
+    r = kv2.kv2_rotary(cs, positions, rot, inter)
+    return lib.kv2_rotary_append(ctypes.byref(c), ctypes.byref(r), K or None, V or None, Q or None, Qo or None, H_q, pos or None,
+                                 start or None, count or None, n, C, ws or None, nb, None)
+
+
+def test_rotary_refusals(lib):
+    c = desc()
+    assert lib.kv2_rotary_append(ctypes.byref(c), None, 0x200, 0x300, None, None, 4, 0x400, 0x500, None, 3, 4, 0x600, 1 << 30,
+                                 None) == 1
+    for rot in (0, 1, 63, 130, -2):
+        assert rotary(lib, c, rot=rot) == 2, rot
+    assert rotary(lib, c, positions=-1) == 1 and rotary(lib, c, inter=2) == 1
+    assert rotary(lib, c, n=-1) == 1 and rotary(lib, c, C=0) == 1 and rotary(lib, c, C=65) == 1
+    assert rotary(lib, c, n=(1 << 30) // 2) == 2                  # rows above 2^30 with two heads
+    assert rotary(lib, c, cs=0) == 1 and rotary(lib, c, cs=0x104) == 1
+    assert rotary(lib, c, K=0) == 1 and rotary(lib, c, V=0x308) == 1
+    assert rotary(lib, c, Q=0x700) == 1 and rotary(lib, c, Q=0x700, Qo=0x708) == 1 and rotary(lib, c, Q=0x700, Qo=0x700, H_q=0) == 1
+    assert rotary(lib, c, pos=0) == 1 and rotary(lib, c, start=0) == 1 and rotary(lib, c, count=0x501) == 1
+    assert rotary(lib, c, ws=0) == 1
+    need = lib.kv2_rotary_append_workspace_size(ctypes.byref(c), 3)
+    assert need == 256 + 256 + 2 * 3 * 2 * 128 * 2 and rotary(lib, c, nb=need - 1) == 6
+    assert rotary(lib, c, n=0) == 0
+    assert rotary(lib, desc(w=0)) == 1
+
+
+def test_rotary_binding_refuses_wrong_tensors():
+    import bit_kv_cache_centroid_b200 as kv2
+    c = kv2.Cache(2, 2, 64, 16, 8, 256, np.zeros((2, 16, 64), np.int16), device="cpu")
+    rot = kv2.Rotary(torch.zeros(10, 64))
+    K = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16)
+    pos, start = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    Q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
+    call = lambda K=K, V=K, pos=pos, start=start, **kw: kv2.kv2_rotary_append(c, rot, K, V, pos, start, 4, **kw)
+    for bad in (dict(K=K[:1]), dict(V=K.float()), dict(pos=pos.long()), dict(pos=pos[:, :2]), dict(start=start[:1]),
+                dict(count=start.long()), dict(Q=Q[:, :2]), dict(Q=Q[0]), dict(Q_out=Q), dict(start=None)):
+        with pytest.raises((ValueError, AttributeError)):
+            call(**bad)
+    with pytest.raises(ValueError):
+        kv2.Rotary(torch.zeros(10, 64, dtype=torch.float64))
+    with pytest.raises(ValueError):
+        kv2.Rotary(torch.zeros(10))
