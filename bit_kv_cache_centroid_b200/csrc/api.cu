@@ -421,10 +421,8 @@ kv2_status check_rows_io(const char* what, const uint16_t* Q, const void* out, i
   return KV2_OK;
 }
 
-// rows per KV head and sequence, and row blocks over the heads, are ints in the kernel
-bool rows_too_many(const kv2_cache* c, int H_q, long long Nq) {
-  return Nq * (H_q / c->H_kv) > (1ll << 30) || Nq * H_q > (1ll << 30);
-}
+// rows are ints in the kernel
+bool rows_too_many(const kv2_cache* c, int H_q, long long Nq) { return Nq * H_q > (1ll << 30) / c->B; }
 
 kv2::RowsArgs cross_args(const kv2_cache* c, const int32_t* lens, int max_len, const int32_t* q_lens, int Nq, int H_q) {
   kv2::RowsArgs a{};
@@ -459,7 +457,7 @@ kv2_status kv2_attention_cross(const kv2_cache* c, const int32_t* lens, int max_
   if (st != KV2_OK) return st;
   if (reinterpret_cast<uintptr_t>(q_lens) & 3u) return fail(KV2_ERR_INVALID_ARG, "cross: q_lens not 4-byte aligned");
   if (Nq < 0) return fail(KV2_ERR_INVALID_ARG, "cross: Nq=%d", Nq);
-  if (rows_too_many(c, H_q, Nq)) return fail(KV2_ERR_UNSUPPORTED, "cross: Nq=%d x H_q=%d above 2^30", Nq, H_q);
+  if (rows_too_many(c, H_q, Nq)) return fail(KV2_ERR_UNSUPPORTED, "cross: %d x Nq=%d x H_q=%d rows above 2^30", c->B, Nq, H_q);
   if (Nq == 0) return ok();
   kv2::RowsArgs a = cross_args(c, lens, max_len, q_lens, Nq, H_q);
   st = check_rows_io("cross", Q, out, out_dtype, ws, ws_bytes, kv2::rows_workspace_bytes(a));
@@ -476,7 +474,7 @@ size_t kv2_attention_shared_workspace_size(const kv2_cache* pre, const kv2_cache
                                            int max_len) {
   if (!pre || !c || H_q <= 0 || c->H_kv <= 0 || H_q % c->H_kv || max_prefix_len < 0 || max_len < 0) return 0;
   if (check_cache(pre, false, false) != KV2_OK || check_cache(c, false, false) != KV2_OK) return 0;
-  if (pre->H_kv != c->H_kv || pre->d != c->d || c->B % pre->B || rows_too_many(c, H_q, c->B)) return 0;
+  if (pre->H_kv != c->H_kv || pre->d != c->d || c->B % pre->B || rows_too_many(c, H_q, 1)) return 0;
   return kv2::rows_workspace_bytes(shared_args(pre, nullptr, max_prefix_len, c, nullptr, max_len, H_q));
 }
 
@@ -492,7 +490,7 @@ kv2_status kv2_attention_shared(const kv2_cache* pre, const int32_t* prefix_lens
     return fail(KV2_ERR_INVALID_ARG, "shared: prefix has %d heads of %d channels, the cache %d of %d", pre->H_kv, pre->d,
                 c->H_kv, c->d);
   if (c->B % pre->B) return fail(KV2_ERR_INVALID_ARG, "shared: %d sequences for %d prefixes", c->B, pre->B);
-  if (rows_too_many(c, H_q, c->B)) return fail(KV2_ERR_UNSUPPORTED, "shared: B=%d x H_q=%d above 2^30", c->B, H_q);
+  if (rows_too_many(c, H_q, 1)) return fail(KV2_ERR_UNSUPPORTED, "shared: B=%d x H_q=%d above 2^30", c->B, H_q);
   kv2::RowsArgs a = shared_args(pre, prefix_lens, max_prefix_len, c, lens, max_len, H_q);
   st = check_rows_io("shared", Q, out, out_dtype, ws, ws_bytes, kv2::rows_workspace_bytes(a));
   if (st != KV2_OK) return st;

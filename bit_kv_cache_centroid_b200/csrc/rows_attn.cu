@@ -64,8 +64,12 @@ namespace {
 
 constexpr int kKeys = 128;             // keys per tile (rows of S^T)
 constexpr float kBias = 7.0f;          // p = 2^(x) with x = s log2e - m + kBias
-constexpr float kTrail = 14.0f;        // x above this refreshes the running maximum
+constexpr float kTrail = 14.0f;        // x above this refreshes the row's running maximum
 constexpr int kStages = 2;
+// A unit begins with kLead positions of the work list that hold no tile: its
+// query rows, first maxima and output rows take about as long as that many key
+// tiles, so parts with many short units get fewer tiles.
+constexpr int kLead = 4;
 
 struct RowsSource {
   const uint32_t* k_code;
@@ -91,8 +95,8 @@ struct RowsParams {
   int out_dtype;
   float scale_log2;
   int* err;
-  long long* total;         // workspace: number of tiles
-  long long* base;          // workspace: first tile of every sequence, [src 0 | src 1]
+  long long* total;         // workspace: length of the work list
+  long long* base;          // workspace: first position of every sequence, [src 0 | src 1]
   int4* cta;                // workspace: {source, sequence, unit in the sequence, first tile in the unit} per CTA
   float* part_o;            // pieces [CTA][2][N][D], slot 0: continues a unit, 1: begins one
   float2* part_ml;          // [CTA][2][N] running maximum and sum
@@ -129,7 +133,8 @@ struct RCfg {
   static constexpr uint32_t OFF_TAB = OFF_SCR + 4 * N * 4;              // per column pair {sc, sc, nm, nm}
   static constexpr uint32_t OFF_MROW = OFF_TAB + N * 8;
   static constexpr uint32_t OFF_ALPHA = OFF_MROW + N * 4;
-  static constexpr uint32_t OFF_RED = OFF_ALPHA + N * 4;                // [X][4 warps][NX]
+  static constexpr uint32_t OFF_ROW = OFF_ALPHA + N * 4;                // row of Q and out per column
+  static constexpr uint32_t OFF_RED = OFF_ROW + N * 4;                  // [X][4 warps][NX]
   static constexpr uint32_t OFF_BAR = OFF_RED + X * 4 * NX * 4;
   static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
   static constexpr uint32_t kTmemUsed = 3 * N;
@@ -178,10 +183,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // ---------------------------------------------------------------------------
-// the tile list
+// the work list: every unit is kLead positions, then one per key tile
 // ---------------------------------------------------------------------------
 
-// first tile of CTA c of C over T tiles, and the CTA that holds tile u
+// first position of CTA c of C over T positions, and the CTA that holds position u
 __device__ __forceinline__ long long part_begin(long long T, int c, int C) { return T * c / C; }
 __device__ __forceinline__ int part_of(long long u, long long T, int C) { return int(((u + 1) * C - 1) / T); }
 
@@ -198,21 +203,21 @@ __device__ __forceinline__ SeqShape seq_shape(const RowsSource& s, int b, int G)
   return q;
 }
 
-// a position in the list; every role of a CTA walks the same segments
+// a place in the list; every role of a CTA walks the same segments
 template <int N>
 struct Walk {
-  long long pos, hi;
-  int src, b, ub, j;
+  long long at, hi;         // position of the unit's first tile, end of the part
+  int src, b, ub, j;        // unit ub of sequence b, next tile j
   SeqShape q;
   __device__ void load(const RowsParams& p) { q = seq_shape<N>(p.src[src], b, p.H_q / p.H_kv); }
-  __device__ bool more() const { return pos < hi; }
-  __device__ int count() const { return int(min(static_cast<long long>(q.nb - j), hi - pos)); }
+  __device__ int count() const { return int(min(static_cast<long long>(q.nb - j), hi - at - j)); }
+  __device__ bool more() const { return at + j < hi; }
   __device__ int head() const { return ub / q.RB; }
   __device__ int block() const { return ub % q.RB; }
   __device__ void next(const RowsParams& p) {
-    pos += count();
+    at += q.nb + kLead;
     j = 0;
-    if (pos >= hi) return;
+    if (at >= hi) return;
     if (++ub < p.H_kv * q.RB) return;
     ub = 0;
     do {
@@ -225,8 +230,8 @@ struct Walk {
   }
 };
 
-// The list's length and this CTA's place in it, by one warp: the tiles of 32
-// sequences at a time, summed by shuffles.
+// The list's length and this CTA's place in it, by one warp: the positions of
+// 32 sequences at a time, summed by shuffles.
 template <int N>
 __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
   const int G = p.H_q / p.H_kv, C = gridDim.x, c = blockIdx.x;
@@ -240,7 +245,7 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
         long long v = 0;
         if (b < p.src[s].B) {
           const SeqShape q = seq_shape<N>(p.src[s], b, G);
-          v = static_cast<long long>(q.nb) * q.RB * p.H_kv;
+          v = static_cast<long long>(q.nb + kLead) * q.RB * p.H_kv;
         }
         long long inc = v;
 #pragma unroll
@@ -258,8 +263,10 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
             w.b = b0 + l;
             const long long rem = lo - (at + __shfl_sync(0xffffffffu, inc - v, l));
             w.load(p);
-            w.ub = int(rem / w.q.nb);
-            w.j = int(rem % w.q.nb);
+            const int unit = w.q.nb + kLead, in = int(rem % unit);
+            w.ub = int(rem / unit);
+            w.j = max(0, in - kLead);
+            w.at = lo - in + kLead;
             found = true;
           }
         }
@@ -269,10 +276,10 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
     if (pass == 0) {
       T = at;
       lo = part_begin(T, c, C);
-      w.pos = lo;
+      w.at = lo;
       w.hi = part_begin(T, c + 1, C);
       if (c == 0 && lane == 0) *p.total = T;
-      if (w.pos >= w.hi) return;
+      if (lo >= w.hi) return;
     }
   }
 }
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
   if (warp == Cfg::kMmaWarp) tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
   if (warp == 0) {
     Walk<N> w;
-    w.pos = w.hi = 0;
+    w.at = w.hi = 0;
     w.src = w.b = w.ub = w.j = 0;
     plan<N>(p, lane, w);
     if (lane == 0) {
@@ -737,6 +744,7 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
     float* tabf = reinterpret_cast<float*>(tab);
     float* mrow = reinterpret_cast<float*>(smem + Cfg::OFF_MROW) + x * NX;
     float* alpha = reinterpret_cast<float*>(smem + Cfg::OFF_ALPHA) + x * NX;
+    int* row_s = reinterpret_cast<int*>(smem + Cfg::OFF_ROW) + x * NX;
     float* red = reinterpret_cast<float*>(smem + Cfg::OFF_RED) + x * 4 * NX;
     auto wait_pv = [&](int tt) {                // P . V of tile tt is complete
       const int pb = PB == 2 ? (tt & 1) : 0;
@@ -803,7 +811,10 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
           bar_sync(bid, 128);
           if (kl < NX) {
             const float tm = fmaxf(fmaxf(red[kl], red[NX + kl]), fmaxf(red[2 * NX + kl], red[3 * NX + kl]));
-            const float mo = mrow[kl], mn = fmaxf(mo, tm);
+            // A whole number: every rescaling is by an exact power of two, and
+            // p's rounding does not depend on where the work is cut. Only the
+            // rows that need it: a row's result does not depend on the others.
+            const float mo = mrow[kl], mn = tm > mo + (kTrail - kBias) ? ceilf(tm) : mo;
             alpha[kl] = mn == -INFINITY ? 1.0f : ex2(mo - mn);
             mrow[kl] = mn;
             // s sc - m is one fma, exact to half a step of m: beyond 2^20 (where
@@ -892,10 +903,6 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
       const bool whole = j0 == 0 && cnt == w.q.nb;
       const int slot = j0 > 0 ? 0 : 1;
       const int r0 = w.block() * N + x * NX, live = min(NX, w.q.ql * G - r0);
-      auto row_of = [&](int c) {                  // row of (sequence, query, head) in Q and out
-        const int ri = r0 + c;
-        return (size_t(w.b) * s.Nq + ri / G) * p.H_q + h * G + ri % G;
-      };
       if (kl < NX) {
         float lt = (red[kl] + red[NX + kl]) + (red[2 * NX + kl] + red[3 * NX + kl]);
         float m = mrow[kl];
@@ -905,8 +912,11 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
         }
         alpha[kl] = lt > 0.0f ? 1.0f / lt : (lt == 0.0f ? 0.0f : lt);
         if (kl < live) {
+          // row of (sequence, query, head) in Q and out
+          const int ri = r0 + kl, row = (w.b * s.Nq + ri / G) * p.H_q + h * G + ri % G;
+          row_s[kl] = row;
           if (!whole) p.part_ml[(size_t(blockIdx.x) * 2 + slot) * N + x * NX + kl] = make_float2(m, lt);
-          else if (!p.out) p.dir_ml[size_t(w.src) * p.dir_rows + row_of(kl)] = make_float2(m, lt);
+          else if (!p.out) p.dir_ml[size_t(w.src) * p.dir_rows + row] = make_float2(m, lt);
         }
       }
       bar_sync(bid, 128);
@@ -928,10 +938,10 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
             if (!whole) {
               p.part_o[((size_t(blockIdx.x) * 2 + slot) * N + x * NX + c) * D + kl] = v[i];
             } else if (!p.out) {
-              p.dir_o[(size_t(w.src) * p.dir_rows + row_of(c)) * D + kl] = v[i];
+              p.dir_o[(size_t(w.src) * p.dir_rows + row_s[c]) * D + kl] = v[i];
             } else {
               const float o = v[i] * alpha[c];
-              const size_t at = row_of(c) * D + kl;
+              const size_t at = size_t(row_s[c]) * D + kl;
               if (p.out_dtype == KV2_OUT_F32) static_cast<float*>(p.out)[at] = o;
               else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
             }
@@ -1027,10 +1037,10 @@ __global__ void __launch_bounds__(256) rows_merge_cut(const __grid_constant__ Ro
   const long long T = *p.total, lo = part_begin(T, c, C);
   if (lo >= part_begin(T, c + 1, C)) return;
   const int4 at = p.cta[c];
-  if (at.w == 0) return;                          // the border lies between units
+  if (at.w == 0) return;                          // no unit is cut here
   const int G = p.H_q / p.H_kv;
   const SeqShape q = seq_shape<N>(p.src[0], at.y, G);
-  const long long u = lo - at.w;
+  const long long u = lo - at.w;                  // position of the unit's first tile
   const int c0 = part_of(u, T, C), c1 = part_of(u + q.nb - 1, T, C);
   if (part_begin(T, c0 + 1, C) != lo) return;     // an earlier border of the same unit
   const int row = blockIdx.y * 8 + warp;
@@ -1059,7 +1069,8 @@ __global__ void __launch_bounds__(256) rows_merge_shared(const __grid_constant__
     const int seq = int(gr / p.H_q), b = seq / src.Nq, i = seq % src.Nq;
     const SeqShape q = seq_shape<N>(src, b, G);
     const int ri = i * G + g;
-    const long long u = p.base[(s ? p.src[0].B : 0) + b] + (static_cast<long long>(h) * q.RB + ri / N) * q.nb;
+    const long long u = p.base[(s ? p.src[0].B : 0) + b] +
+                        (static_cast<long long>(h) * q.RB + ri / N) * (q.nb + kLead) + kLead;
     const int c0 = part_of(u, T, C), c1 = part_of(u + q.nb - 1, T, C);
     if (c0 == c1) {
       const float2 ml = p.dir_ml[size_t(s) * p.dir_rows + gr];

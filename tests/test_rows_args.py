@@ -47,7 +47,7 @@ def test_cross_refusals(lib):
     assert cross(lib, c, max_len=-1) == 3
     assert cross(lib, c, lens=0x1002) == 1 and cross(lib, c, q_lens=0x1001) == 1
     assert cross(lib, c, Nq=-1) == 1
-    assert cross(lib, c, Nq=(1 << 30) // 4 + 1) == 2
+    assert cross(lib, c, Nq=(1 << 30) // 8 + 1) == 2                 # rows above 2^30
     assert cross(lib, c, Q=0) == 1 and cross(lib, c, Q=0x108) == 1 and cross(lib, c, out=0x204) == 1
     assert cross(lib, c, dt=2) == 1 and cross(lib, c, ws=0) == 1
     need = lib.kv2_attention_cross_workspace_size(ctypes.byref(c), 4, 3, 256)
