@@ -107,18 +107,20 @@ struct RowsParams {
   int force_timeout;
 };
 
-// D channels, X groups of NX rows (columns of S^T), N = X * NX rows per unit
-template <int D, int NX, int X>
+// D channels, N rows per unit (columns of S^T)
+template <int D, int NT>
 struct RCfg {
-  static constexpr int N = NX * X;
-  // producer threads per key: few rows are bound by dequantization, and 16
-  // warps hide its latency best; with 64 columns the softmax threads' sums
-  // need the registers
-  static constexpr int TPR = NX <= 32 ? 4 : 2;
-  static constexpr int PW = kKeys * TPR / 32, SW = 4 * X, kMmaWarp = SW + PW;
-  static constexpr int kThreads = 32 * (SW + PW + 1);
+  static constexpr int N = NT;
+  static constexpr int X = N == 128 ? 2 : 1, NX = N / X;       // MMA groups of NX columns
+  // softmax: 128 threads (keys) per group of CPT columns, so that a thread's
+  // sums stay in registers
+  static constexpr int CPT = N <= 32 ? 16 : 32, SG = N / CPT, SW = 4 * SG;
+  // producers: 4 threads per key (16 warps hide the loads' latency); at 128
+  // rows, where the softmax has 16 warps, 2
+  static constexpr int TPR = N == 128 ? 2 : 4, PW = kKeys * TPR / 32;
+  static constexpr int kMmaWarp = SW + PW, kThreads = 32 * (SW + PW + 1);
   static constexpr int CH = D / TPR;                 // channels per producer thread
-  static constexpr int PB = X == 1 ? 2 : 1;          // P buffers per group
+  static constexpr int PB = X == 1 ? 2 : 1;          // P buffers per MMA group
   static constexpr int Q_BYTES = NX * D * 2, U_BYTES = NX * 32, K_BYTES = kKeys * D * 2, A_BYTES = kKeys * 32;
   static constexpr int V_BYTES = kKeys * 256;        // 128 channels (zero above D)
   static constexpr int P_BYTES = NX * 256;
@@ -130,12 +132,13 @@ struct RCfg {
   static constexpr uint32_t OFF_U = OFF_A + kStages * A_BYTES;
   static constexpr uint32_t OFF_FRAG = OFF_U + X * U_BYTES;             // P fragments [D/16][2][2][32] uint2
   static constexpr uint32_t OFF_SCR = OFF_FRAG + D / 16 * 2 * 2 * 32 * 8;   // row scales, ring of 4 units
-  static constexpr uint32_t OFF_TAB = OFF_SCR + 4 * N * 4;              // per column pair {sc, sc, nm, nm}
+  static constexpr uint32_t OFF_QE = OFF_SCR + 4 * N * 4;               // row exponents of the unit being loaded
+  static constexpr uint32_t OFF_TAB = OFF_QE + N * 4;                   // per column pair {sc, sc, nm, nm}
   static constexpr uint32_t OFF_MROW = OFF_TAB + N * 8;
   static constexpr uint32_t OFF_ALPHA = OFF_MROW + N * 4;
   static constexpr uint32_t OFF_ROW = OFF_ALPHA + N * 4;                // row of Q and out per column
-  static constexpr uint32_t OFF_RED = OFF_ROW + N * 4;                  // [X][4 warps][NX]
-  static constexpr uint32_t OFF_BAR = OFF_RED + X * 4 * NX * 4;
+  static constexpr uint32_t OFF_RED = OFF_ROW + N * 4;                  // [SG][4 warps][CPT]
+  static constexpr uint32_t OFF_BAR = OFF_RED + 4 * N * 4;
   static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
   static constexpr uint32_t kTmemUsed = 3 * N;
   static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
@@ -143,12 +146,12 @@ struct RCfg {
   static constexpr uint32_t kIdQK = make_idesc(0, 0, 0, NX, kKeys);
   static constexpr uint32_t kIdPV = make_idesc(0, 0, NX == 64 ? 1 : 0, NX, 128, 1);
   static_assert(SMEM <= 232448, "shared memory of one CTA");
-  static_assert(NX == 16 || NX == 32 || NX == 64, "columns per group");
+  static_assert(N == 16 || N == 32 || N == 64 || N == 128, "rows per unit");
 };
 // barrier slots (bytes from OFF_BAR)
 constexpr uint32_t B_KFULL = 0, B_KEMPTY = 16, B_VFULL = 32, B_VEMPTY = 48, B_SFULL = 64, B_SFREE = 96,
                    B_PFULL = 128, B_PDONE = 160, B_QFULL = 192, B_QEMPTY = 200, B_FINAL = 208, B_NEVER = 216,
-                   B_TMEM = 224, B_ABORT = 228, B_PMAX = 232;
+                   B_TMEM = 224, B_ABORT = 228;
 
 // order-preserving map of floats to signed integers, and back
 __device__ __forceinline__ int f2ord(float x) {
@@ -174,12 +177,29 @@ __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
+// d += A B, m16n8k16, bf16 operands, fp32 sums
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 bytes global -> shared by the asynchronous copy (zeros when !ok)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// e with |x| < 2^e (finite x; -126 at least), and 2^e
+__device__ __forceinline__ int exp_above(float x) { return int((__float_as_uint(x) >> 23) & 0xffu) - 126; }
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// a += the two fp16 values of w
+__device__ __forceinline__ void add_f16x2(float& a, float& b, uint32_t w) {
+  asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}\n"
+      : "+f"(a), "+f"(b)
+      : "r"(w));
 }
 
 // ---------------------------------------------------------------------------
@@ -190,43 +210,47 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ long long part_begin(long long T, int c, int C) { return T * c / C; }
 __device__ __forceinline__ int part_of(long long u, long long T, int C) { return int(((u + 1) * C - 1) / T); }
 
-struct SeqShape {
-  int len, ql, nb, RB;      // keys, queries, tiles per unit, row blocks
-};
-template <int N>
-__device__ __forceinline__ SeqShape seq_shape(const RowsSource& s, int b, int G) {
-  SeqShape q;
-  q.len = s.lens ? min(max(s.lens[b], 0), s.max_len) : s.max_len;
-  q.ql = s.q_lens ? min(max(s.q_lens[b], 0), s.Nq) : s.Nq;
-  q.nb = max(1, (q.len + kKeys - 1) / kKeys);     // an empty sequence has one masked tile: its rows become zero
-  q.RB = (q.ql * G + N - 1) / N;                  // (rows fit in 30 bits)
-  return q;
+// keys and queries of a sequence
+__device__ __forceinline__ int seq_len(const RowsSource& s, int b) {
+  return s.lens ? min(max(s.lens[b], 0), s.max_len) : s.max_len;
 }
+__device__ __forceinline__ int seq_queries(const RowsSource& s, int b) {
+  return s.q_lens ? min(max(s.q_lens[b], 0), s.Nq) : s.Nq;
+}
+// tiles per unit (an empty sequence has one masked tile: its rows become zero)
+// and row blocks of a sequence (its rows fit in 30 bits)
+__device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kKeys - 1) / kKeys); }
+template <int N>
+__device__ __forceinline__ int blocks_of(int ql, int G) { return (ql * G + N - 1) / N; }
 
 // a place in the list; every role of a CTA walks the same segments
 template <int N>
 struct Walk {
-  long long at, hi;         // position of the unit's first tile, end of the part
-  int src, b, ub, j;        // unit ub of sequence b, next tile j
-  SeqShape q;
-  __device__ void load(const RowsParams& p) { q = seq_shape<N>(p.src[src], b, p.H_q / p.H_kv); }
-  __device__ int count() const { return int(min(static_cast<long long>(q.nb - j), hi - at - j)); }
-  __device__ bool more() const { return at + j < hi; }
-  __device__ int head() const { return ub / q.RB; }
-  __device__ int block() const { return ub % q.RB; }
+  int left;                 // positions from the unit's first tile to the part's end
+  int src, b, h, rb, j;     // row block rb of KV head h of sequence b, next tile j
+  int len, ql;
+  __device__ void load(const RowsParams& p) {
+    len = seq_len(p.src[src], b);
+    ql = seq_queries(p.src[src], b);
+  }
+  __device__ int count() const { return min(tiles_of(len), left) - j; }
+  __device__ bool more() const { return j < left; }
   __device__ void next(const RowsParams& p) {
-    at += q.nb + kLead;
+    left -= tiles_of(len) + kLead;
     j = 0;
-    if (at >= hi) return;
-    if (++ub < p.H_kv * q.RB) return;
-    ub = 0;
+    if (left <= 0) return;
+    const int G = p.H_q / p.H_kv;
+    if (++rb < blocks_of<N>(ql, G)) return;
+    rb = 0;
+    if (++h < p.H_kv) return;
+    h = 0;
     do {
       if (++b == p.src[src].B) {
         b = 0;
         ++src;
       }
       load(p);
-    } while (q.RB == 0);
+    } while (ql == 0);
   }
 };
 
@@ -235,7 +259,7 @@ struct Walk {
 template <int N>
 __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
   const int G = p.H_q / p.H_kv, C = gridDim.x, c = blockIdx.x;
-  long long T = 0, lo = 0;
+  long long T = 0, lo = 0, hi = 0;
   for (int pass = 0; pass < 2; ++pass) {
     long long at = 0;
     bool found = false;
@@ -244,8 +268,8 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
         const int b = b0 + lane;
         long long v = 0;
         if (b < p.src[s].B) {
-          const SeqShape q = seq_shape<N>(p.src[s], b, G);
-          v = static_cast<long long>(q.nb + kLead) * q.RB * p.H_kv;
+          v = static_cast<long long>(tiles_of(seq_len(p.src[s], b)) + kLead) *
+              blocks_of<N>(seq_queries(p.src[s], b), G) * p.H_kv;
         }
         long long inc = v;
 #pragma unroll
@@ -263,10 +287,12 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
             w.b = b0 + l;
             const long long rem = lo - (at + __shfl_sync(0xffffffffu, inc - v, l));
             w.load(p);
-            const int unit = w.q.nb + kLead, in = int(rem % unit);
-            w.ub = int(rem / unit);
+            const int unit = tiles_of(w.len) + kLead, in = int(rem % unit), ub = int(rem / unit);
+            const int RB = blocks_of<N>(w.ql, G);
+            w.h = ub / RB;
+            w.rb = ub % RB;
             w.j = max(0, in - kLead);
-            w.at = lo - in + kLead;
+            w.left = int(hi - (lo - in + kLead));
             found = true;
           }
         }
@@ -276,10 +302,9 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
     if (pass == 0) {
       T = at;
       lo = part_begin(T, c, C);
-      w.at = lo;
-      w.hi = part_begin(T, c + 1, C);
+      hi = part_begin(T, c + 1, C);
       if (c == 0 && lane == 0) *p.total = T;
-      if (lo >= w.hi) return;
+      if (lo >= hi) return;
     }
   }
 }
@@ -288,64 +313,84 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
 // producers
 // ---------------------------------------------------------------------------
 
-// packed fields of CH channels of a cached token, channels part * CH ..
-template <int CH>
-struct Raw {
-  static constexpr int W = CH / 16, Z = CH >= 64 ? 2 : 1;
-  uint32_t kw[W], vw[W], ksz[Z], vsz[Z];
+// Packed fields of CH channels of a cached token, channels part * CH ..; of
+// its key also the centre's id and 16 / TPR PSAC coefficients (fp16, or int8
+// codes and the token's scale in the last word).
+template <int CH, int TPR>
+struct KRaw {
+  static constexpr int W = CH / 16, Z = CH >= 64 ? 2 : 1, CP = 16 / TPR;
+  uint32_t w[W], z[Z], ps[CP / 2];
   int idx;
+};
+template <int CH>
+struct VRaw {
+  static constexpr int W = CH / 16, Z = CH >= 64 ? 2 : 1;
+  uint32_t w[W], z[Z];
 };
 
 template <int W>
-__device__ __forceinline__ void load_words(const uint32_t* src, uint32_t (&w)[W]) {
+__device__ __forceinline__ void load_words(const void* src, uint32_t (&w)[W]) {
   if constexpr (W == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    const uint4 v = *static_cast<const uint4*>(src);
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   } else if constexpr (W == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    const uint2 v = *static_cast<const uint2*>(src);
     w[0] = v.x; w[1] = v.y;
   } else {
-    w[0] = *src;
+    w[0] = *static_cast<const uint32_t*>(src);
   }
 }
-
-template <int D, int CH>
-__device__ __forceinline__ void load_raw(const RowsSource& s, size_t slot, int part, Raw<CH>& r) {
-  load_words<CH / 16>(s.k_code + slot * (D / 16) + part * (CH / 16), r.kw);
-  load_words<CH / 16>(s.v_code + slot * (D / 16) + part * (CH / 16), r.vw);
-  const size_t z = slot * (D >> s.gshift);
+template <int D, int CH, int Z>
+__device__ __forceinline__ void load_sz(const uint32_t* sz, size_t slot, int gshift, int part, uint32_t (&z)[Z]) {
+  const uint32_t* row = sz + slot * (D >> gshift);
 #pragma unroll
-  for (int i = 0; i < Raw<CH>::Z; ++i) {
-    const int g = (part * CH + 32 * i) >> s.gshift;
-    r.ksz[i] = s.k_sz[z + g];
-    r.vsz[i] = s.v_sz[z + g];
-  }
+  for (int i = 0; i < Z; ++i) z[i] = row[(part * CH + 32 * i) >> gshift];
+}
+
+template <int D, int CH, int TPR>
+__device__ __forceinline__ void load_key(const RowsSource& s, size_t slot, int part, KRaw<CH, TPR>& r) {
+  constexpr int CP = KRaw<CH, TPR>::CP;
   r.idx = (s.M <= 256) ? int(static_cast<const uint8_t*>(s.cidx)[slot]) : int(static_cast<const uint16_t*>(s.cidx)[slot]);
+  load_words(s.k_code + slot * (D / 16) + part * (CH / 16), r.w);
+  load_sz<D, CH>(s.k_sz, slot, s.gshift, part, r.z);
+#pragma unroll
+  for (int i = 0; i < CP / 2; ++i) r.ps[i] = 0u;
+  if (part * CP < s.r) {
+    if (s.psac_fmt == 1) {
+      uint32_t q[CP / 4];
+      load_words(reinterpret_cast<const int8_t*>(s.psac) + slot * s.r + part * CP, q);
+#pragma unroll
+      for (int i = 0; i < CP / 4; ++i) r.ps[i] = q[i];
+      r.ps[CP / 2 - 1] = s.psac_scale[slot];
+    } else {
+      load_words(s.psac + slot * s.r + part * CP, r.ps);
+    }
+  }
+}
+template <int D, int CH>
+__device__ __forceinline__ void load_value(const RowsSource& s, size_t slot, int part, VRaw<CH>& r) {
+  load_words(s.v_code + slot * (D / 16) + part * (CH / 16), r.w);
+  load_sz<D, CH>(s.v_sz, slot, s.gshift, part, r.z);
 }
 
-// the PSAC row of a cached token (fp16, zero-padded to 16 coefficients)
-__device__ __forceinline__ void load_psac(const RowsSource& s, size_t slot, uint4& a0, uint4& a1) {
-  a0 = a1 = make_uint4(0, 0, 0, 0);
-  if (s.r == 0) return;
-  if (s.psac_fmt == 1) {
-    // int8 codes and the token's scale: fp16(code * scale)
-    const float sc = __half2float(__ushort_as_half(s.psac_scale[slot]));
-    const int8_t* q8 = reinterpret_cast<const int8_t*>(s.psac) + slot * s.r;
-    const uint2 lo = *reinterpret_cast<const uint2*>(q8);
-    const uint2 hi = s.r >= 16 ? *reinterpret_cast<const uint2*>(q8 + 8) : make_uint2(0, 0);
-    const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
-    uint32_t h[8];
+// the part's PSAC coefficients as fp16 into the operand row (int8: fp16(code * scale))
+template <int CH, int TPR>
+__device__ __forceinline__ void store_psac(const KRaw<CH, TPR>& r, bool int8, bool have, int row, int part, uint8_t* tile) {
+  constexpr int CP = KRaw<CH, TPR>::CP;
+  uint32_t a[CP / 2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t two = (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-      h[i] = pack_f16(float(int8_t(two & 0xff)) * sc, float(int8_t(two >> 8)) * sc);
+  for (int i = 0; i < CP / 2; ++i) a[i] = have ? r.ps[i] : 0u;
+  if (int8 && have) {
+    const float sc = __half2float(__ushort_as_half(uint16_t(r.ps[CP / 2 - 1])));
+#pragma unroll
+    for (int i = 0; i < CP / 2; ++i) {
+      const uint32_t two = (r.ps[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+      a[i] = pack_f16(float(int8_t(two & 0xff)) * sc, float(int8_t(two >> 8)) * sc);
     }
-    a0 = make_uint4(h[0], h[1], h[2], h[3]);
-    a1 = make_uint4(h[4], h[5], h[6], h[7]);
-    return;
   }
-  a0 = *reinterpret_cast<const uint4*>(s.psac + slot * s.r);
-  if (s.r >= 16) a1 = *reinterpret_cast<const uint4*>(s.psac + slot * s.r + 8);
+  uint8_t* dst = tile + nosw_off(row, part * CP / 8) + (part * CP % 8) * 2;
+  if constexpr (CP == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
+  else *reinterpret_cast<uint2*>(dst) = make_uint2(a[0], a[1]);
 }
 
 __device__ __forceinline__ uint4 dequant8(uint32_t word, int lc, uint32_t s2, const uint32_t (&add)[4]) {
@@ -357,50 +402,33 @@ __device__ __forceinline__ uint4 dequant8(uint32_t word, int lc, uint32_t s2, co
 }
 
 // ---------------------------------------------------------------------------
-// column sums over the warp's lanes (keys): afterwards lane c % 32 holds
-// column c's sum in v[c / 32] (N = 16: lanes c and c + 16)
+// column sums over the warp's lanes (keys): afterwards lane c holds column c's
+// sum in v[0] (16 columns: lanes c and c + 16)
 // ---------------------------------------------------------------------------
 template <int NX>
 __device__ __forceinline__ void warp_colsum(float (&v)[NX], int lane) {
-  constexpr int S = NX < 32 ? NX : 32;
+  static_assert(NX == 16 || NX == 32, "columns");
   if constexpr (NX == 16) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
   }
 #pragma unroll
-  for (int h = 0; h < NX; h += S) {
+  for (int o = NX / 2; o > 0; o >>= 1) {
 #pragma unroll
-    for (int o = S / 2; o > 0; o >>= 1) {
-#pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const float a = v[h + i], b = v[h + i + o];
-        const bool up = (lane & o) != 0;
-        v[h + i] = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, o);
-      }
+    for (int i = 0; i < o; ++i) {
+      const float a = v[i], b = v[i + o];
+      const bool up = (lane & o) != 0;
+      v[i] = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, o);
     }
-    v[h / S] = v[h];
-  }
-}
-
-template <int CW>
-__device__ __forceinline__ void tmem_cols(uint32_t t, float (&v)[CW]) {
-  if constexpr (CW == 16) {
-    tmem_ld16(t, v);
-  } else {
-    uint32_t r[32];
-    tmem_ld32_issue(t, r);
-    tmem_wait_ld(r);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
   }
 }
 
 // ---------------------------------------------------------------------------
-template <int D, int NX, int X>
-__global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsParams p) {
-  using Cfg = RCfg<D, NX, X>;
-  constexpr int N = Cfg::N, SW = Cfg::SW, PW = Cfg::PW, PB = Cfg::PB, CH = Cfg::CH;
-  constexpr int CW = NX < 32 ? NX : 32;
+template <int D, int NT>
+__global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsParams p) {
+  using Cfg = RCfg<D, NT>;
+  constexpr int N = Cfg::N, X = Cfg::X, NX = Cfg::NX, SW = Cfg::SW, PW = Cfg::PW, PB = Cfg::PB;
+  constexpr int CH = Cfg::CH, TPR = Cfg::TPR, CPT = Cfg::CPT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -412,7 +440,7 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.H_q / p.H_kv;
 
-  if (tid == 0) {
+  if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar + B_KFULL + 8 * i, PW * 32);
       mbar_init(bar + B_KEMPTY + 8 * i, 1);
@@ -420,9 +448,9 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
       mbar_init(bar + B_VEMPTY + 8 * i, 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar + B_SFULL + 8 * i, 1);          // [group][buffer]
-      mbar_init(bar + B_SFREE + 8 * i, 128);
-      mbar_init(bar + B_PFULL + 8 * i, 128);
+      mbar_init(bar + B_SFULL + 8 * i, 1);          // [MMA group][buffer]
+      mbar_init(bar + B_SFREE + 8 * i, SW * 32 / X);
+      mbar_init(bar + B_PFULL + 8 * i, SW * 32 / X);
       mbar_init(bar + B_PDONE + 8 * i, 1);
     }
     mbar_init(bar + B_QFULL, PW * 32);
@@ -435,12 +463,11 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
   if (warp == Cfg::kMmaWarp) tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
   if (warp == 0) {
     Walk<N> w;
-    w.at = w.hi = 0;
-    w.src = w.b = w.ub = w.j = 0;
+    w.left = w.src = w.b = w.h = w.rb = w.j = w.len = w.ql = 0;
     plan<N>(p, lane, w);
     if (lane == 0) {
       walk_s = w;
-      p.cta[blockIdx.x] = make_int4(w.src, w.b, w.ub, w.j);
+      p.cta[blockIdx.x] = make_int4(w.src, w.b, w.h * blocks_of<N>(w.ql, G) + w.rb, w.j);
     }
   }
   if constexpr (D < 128) {
@@ -467,8 +494,8 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
     const uint64_t dP = make_sdesc(sb + Cfg::OFF_P, NX == 64 ? 16384 : 16, 1024, kLayoutSW128);
     bool ok = true;
     int t = 0, seg = 0;
-    // P . V of tile t (the first of its unit's part starts the sums afresh)
-    auto issue_pv = [&](int tt, bool first) -> bool {
+    // P . V of tile tt (the first of its unit's part starts the sums afresh)
+    auto issue_pv = [&](int tt, bool first) __attribute__((always_inline)) -> bool {
       const int s = tt & 1;
       if (!mbar_wait_or_abort(bar + B_VFULL + 8 * s, (tt >> 1) & 1, p.budget, abort)) return false;
       for (int x = 0; x < X; ++x) {
@@ -540,350 +567,353 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
     // lanes 8q..8q+7 of a warp take 8 consecutive keys and one part of their
     // channels: their 16-byte stores fall on 8 distinct swizzled bank groups
     const int pt = tid - SW * 32, pw = pt >> 5;
-    const int row = Cfg::TPR == 4 ? pw * 8 + (lane & 7) : pw * 16 + (lane & 7) + 8 * (lane >> 4);
-    const int part = Cfg::TPR == 4 ? lane >> 3 : (lane >> 3) & 1;
+    const int row = TPR == 4 ? pw * 8 + (lane & 7) : pw * 16 + (lane & 7) + 8 * (lane >> 4);
+    const int part = TPR == 4 ? lane >> 3 : (lane >> 3) & 1;
     uint2* frag = reinterpret_cast<uint2*>(smem + Cfg::OFF_FRAG);
-    uint32_t* pmax_s = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAR + B_PMAX);
     int t = 0, seg = 0, frag_src = -1, frag_h = -1;
-    float pmax = 0.0f;
-    for (; w.more(); ++seg) {
-      const RowsSource& s = p.src[w.src];
-      const int cnt = w.count(), h = w.head(), j0 = w.j, len = w.q.len;
-      // ---- fragments of P (fp16 halves of P 2^e, max |P| 2^e in [2^13, 2^14)) for U = Q P
-      if (s.r > 0 && (w.src != frag_src || h != frag_h)) {
+
+    // The query rows of a unit, warp g rows 16 g .. 16 g + 15: copied raw, their
+    // product with the basis (bf16 query, exact; P as two bf16 numbers, 2^-16),
+    // then both scaled by 2^e per row, max(|q|, |u|) 2^e < 2^15, to fp16.
+    auto load_queries = [&](int src, int b, int h, int rb, int ql) __attribute__((always_inline)) {
+      const RowsSource& s = p.src[src];
+      if (s.r > 0 && (src != frag_src || h != frag_h)) {
         const float* Ph = s.P + size_t(h) * D * s.r;
-        constexpr int TASKS = D / 16 * 2 * 32, PER = (TASKS + PW * 32 - 1) / (PW * 32);
-        float v[PER][4];
-        float mx = 0.0f;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          const int i = pt + k * PW * 32, l = i & 31, nt = (i >> 5) & 1, ks = i >> 6;
+        bar_sync(1, PW * 32);                     // the previous fragments are read
+        for (int i = pt; i < D / 16 * 2 * 32; i += PW * 32) {
+          const int l = i & 31, nt = (i >> 5) & 1, ks = i >> 6;
           const int n = nt * 8 + (l >> 2), c = ks * 16 + 2 * (l & 3);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[k][e] = (i < TASKS && n < s.r) ? Ph[size_t(c + (e & 1) + 8 * (e >> 1)) * s.r + n] : 0.0f;
-            mx = fmaxf(mx, fabsf(v[k][e]));
-          }
-        }
-        bar_sync(1, PW * 32);                     // the previous fragments and maximum are read
-        if (pt == 0) *pmax_s = 0;
-        bar_sync(1, PW * 32);
-        const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-        if (lane == 0) atomicMax(pmax_s, wm);
-        bar_sync(1, PW * 32);
-        pmax = __uint_as_float(*pmax_s);
-        int e2 = 0;
-        if (pmax > 0.0f && pmax < 1e30f) frexpf(pmax, &e2);
-        const float mul = ldexpf(1.0f, 14 - e2);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          const int i = pt + k * PW * 32, l = i & 31, nt = (i >> 5) & 1, ks = i >> 6;
-          if (i >= TASKS) break;
           float hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float y = v[k][e] * mul;
-            hi[e] = __half2float(__float2half_rn(y));
+            const float y = n < s.r ? __ldg(Ph + size_t(c + (e & 1) + 8 * (e >> 1)) * s.r + n) : 0.0f;
+            hi[e] = __bfloat162float(__float2bfloat16_rn(y));
             lo[e] = y - hi[e];
           }
-          frag[((ks * 2 + nt) * 2 + 0) * 32 + l] = make_uint2(pack_f16(hi[0], hi[1]), pack_f16(hi[2], hi[3]));
-          frag[((ks * 2 + nt) * 2 + 1) * 32 + l] = make_uint2(pack_f16(lo[0], lo[1]), pack_f16(lo[2], lo[3]));
+          frag[((ks * 2 + nt) * 2 + 0) * 32 + l] = make_uint2(pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3]));
+          frag[((ks * 2 + nt) * 2 + 1) * 32 + l] = make_uint2(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]));
         }
         bar_sync(1, PW * 32);
-        frag_src = w.src;
+        frag_src = src;
         frag_h = h;
       }
-      // ---- query rows of the unit: warp g takes rows 16 g .. 16 g + 15
-      // scale 2^e per row: |q| 2^e < 2^15 and |u| = |q P| <= D max|q| max|P| likewise
       if (pw < N / 16) {
         constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;     // lanes per row, rows per step, steps
-        const int c = lane % LPR;
-        uint4 v[IT];
+        const int c = lane % LPR, x = pw * 16 / NX, r0 = pw * 16 % NX;
+        uint8_t* qt = smem + Cfg::OFF_Q + x * Cfg::Q_BYTES;
+        auto q_off = [&](int rx, int ck) { return (ck >> 3) * NX * 128 + rx * 128 + (((ck & 7) ^ (rx & 7)) << 4); };
+        if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-          const int rr = pw * 16 + k * RPI + lane / LPR;
-          const int ri = w.block() * N + rr;
-          v[k] = make_uint4(0, 0, 0, 0);
-          if (ri < w.q.ql * G) {
-            const size_t gr = (size_t(w.b) * s.Nq + ri / G) * p.H_q + h * G + ri % G;
-            v[k] = __ldg(reinterpret_cast<const uint4*>(p.Q + gr * D) + c);
+          const int rx = r0 + k * RPI + lane / LPR, ri = rb * N + x * NX + rx;
+          const bool in = ri < ql * G;
+          const size_t gr = in ? (size_t(b) * s.Nq + ri / G) * p.H_q + h * G + ri % G : 0;
+          copy16(sb + Cfg::OFF_Q + x * Cfg::Q_BYTES + q_off(rx, c), p.Q + gr * D + c * 8, in);
+        }
+        float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + pw * 16;
+        int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE) + pw * 16;
+        copy_wait();
+        __syncwarp();
+        float acc[2][4] = {};
+        if (s.r > 0) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t a[4];
+            ldsm_x4(a, sb + Cfg::OFF_Q + x * Cfg::Q_BYTES + q_off(r0 + (lane & 15), 2 * ks + (lane >> 4)));
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                const uint2 bb = frag[((ks * 2 + nt) * 2 + hl) * 32 + lane];
+                mma16816(acc[nt], a, bb.x, bb.y);
+              }
           }
         }
-        if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
-        float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N;
-        int room = 0;                             // max(1, D max|P|) <= 2^room
-        if (s.r > 0 && pmax > 0.0f && pmax < 1e30f) frexpf(fmaxf(1.0f, pmax * float(D)), &room);
+        // largest |u| of rows lane / 4 and lane / 4 + 8, for the lanes that scale them
+        float u0 = fmaxf(fmaxf(fabsf(acc[0][0]), fabsf(acc[0][1])), fmaxf(fabsf(acc[1][0]), fabsf(acc[1][1])));
+        float u1 = fmaxf(fmaxf(fabsf(acc[0][2]), fabsf(acc[0][3])), fmaxf(fabsf(acc[1][2]), fabsf(acc[1][3])));
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
+          u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
+        }
+        if ((lane & 3) == 0) {
+          scr[lane >> 2] = u0;
+          scr[(lane >> 2) + 8] = u1;
+        }
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-          const int rr = pw * 16 + k * RPI + lane / LPR;
-          const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          const int rr = k * RPI + lane / LPR;
+          uint4* at = reinterpret_cast<uint4*>(qt + q_off(r0 + rr, c));
+          const uint4 v = *at;
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
           uint32_t am = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) am = __vmaxu2(am, u[i] & 0x7fff7fffu);
           am = max(am & 0xffffu, am >> 16);
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-          int qexp = 0;
-          if (am > 0 && am < 0x7f80u) {           // a finite row
-            int e = 0;
-            frexpf(__uint_as_float(am << 16), &e);
-            qexp = min(max(15 - e - room, -126), 64);
-          }
-          const float qmul = ldexpf(1.0f, qexp);
+          const float top = fmaxf(__uint_as_float(am << 16), scr[rr]);
+          const int e = top > 0.0f && top < INFINITY && am < 0x7f80u ? min(max(15 - exp_above(top), -126), 64) : 0;
+          const float qmul = pow2(e);
           uint32_t o4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             o4[i] = pack_f16(__uint_as_float(u[i] << 16) * qmul, __uint_as_float(u[i] & 0xffff0000u) * qmul);
-          const int x = rr / NX, rx = rr % NX;
-          *reinterpret_cast<uint4*>(smem + Cfg::OFF_Q + x * Cfg::Q_BYTES + (c >> 3) * NX * 128 + rx * 128 +
-                                    (((c & 7) ^ (rx & 7)) << 4)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-          if (c == 0) scr[rr] = p.scale_log2 * ldexpf(1.0f, -qexp);
+          *at = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+          if (c == 0) qe[rr] = e;
         }
         __syncwarp();
+        if (lane < 16) scr[lane] = p.scale_log2 * pow2(-qe[lane]);
         if (s.r > 0) {
-          // U = Q P of the warp's 16 rows: fp16 query, fp16 halves of P, fp32 sums
-          const int x = pw * 16 / NX, r0 = pw * 16 % NX;
-          const uint32_t qb = sb + Cfg::OFF_Q + x * Cfg::Q_BYTES;
-          float acc[2][4] = {};
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const int rx = r0 + (lane & 15), ck = 2 * ks + (lane >> 4);
-            uint32_t a[4];
-            ldsm_x4(a, qb + (ck >> 3) * NX * 128 + rx * 128 + (((ck & 7) ^ (rx & 7)) << 4));
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-              for (int hl = 0; hl < 2; ++hl) {
-                const uint2 bb = frag[((ks * 2 + nt) * 2 + hl) * 32 + lane];
-                mma16816(acc[nt], a, bb.x, bb.y);
-              }
-          }
-          int e2 = 0;
-          if (pmax > 0.0f && pmax < 1e30f) frexpf(pmax, &e2);
-          const float back = ldexpf(1.0f, e2 - 14);
           uint8_t* ut = smem + Cfg::OFF_U + x * Cfg::U_BYTES;
+          const int ra = lane >> 2, q = (lane & 3) * 4;
+          const float ma = pow2(qe[ra]), mb = pow2(qe[ra + 8]);
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
-            const int ra = r0 + (lane >> 2), q = (lane & 3) * 4;
-            *reinterpret_cast<uint32_t*>(ut + nosw_off(ra, nt) + q) = pack_f16(acc[nt][0] * back, acc[nt][1] * back);
-            *reinterpret_cast<uint32_t*>(ut + nosw_off(ra + 8, nt) + q) = pack_f16(acc[nt][2] * back, acc[nt][3] * back);
+            *reinterpret_cast<uint32_t*>(ut + nosw_off(r0 + ra, nt) + q) = pack_f16(acc[nt][0] * ma, acc[nt][1] * ma);
+            *reinterpret_cast<uint32_t*>(ut + nosw_off(r0 + ra + 8, nt) + q) = pack_f16(acc[nt][2] * mb, acc[nt][3] * mb);
           }
         }
       }
       fence_proxy_async();
       mbar_arrive(bar + B_QFULL);
+    };
 
-      // ---- key and value tiles; the packed fields are loaded one tile ahead
-      const uint4* cent4 = reinterpret_cast<const uint4*>(s.cent) + size_t(h) * s.M * (D / 8) + part * (CH / 8);
-      auto slot_of = [&](int tok) { return cache_slot(s.table, s.page, p.H_kv, s.cap, w.b, h, tok); };
-      Raw<CH> raw;
-      bool have = j0 * kKeys + row < len;
-      if (have) load_raw<D, CH>(s, slot_of(j0 * kKeys + row), part, raw);
-      for (int jj = 0; jj < cnt; ++jj, ++t) {
-        const int st = t & 1;
-        uint4 mu[CH / 8], a0, a1;
+    // Tile by tile: the centre rows of tile t (their ids arrived with the
+    // packed key a tile ago) and the packed fields of the next are requested,
+    // the values of tile t - 1 are written meanwhile, then the keys of tile t.
+    KRaw<CH, TPR> k;
+    VRaw<CH> v;
+    size_t slot = 0;
+    bool kh = false, vh = false;                // the thread's token of tile t (t - 1) exists
+    auto open_tile = [&](KRaw<CH, TPR>& r) __attribute__((always_inline)) {
+      const RowsSource& s = p.src[w.src];
+      const int tok = w.j * kKeys + row;
+      if (tok >= w.len) return false;
+      slot = cache_slot(s.table, s.page, p.H_kv, s.cap, w.b, w.h, tok);
+      load_key<D, CH, TPR>(s, slot, part, r);
+      return true;
+    };
+    bool run = w.more(), first = true;
+    if (run) kh = open_tile(k);
+#pragma unroll 1
+    while (run || t > 0) {                       // one round more than tiles: the last tile's values
+      uint4 mu[CH / 8];
+      KRaw<CH, TPR> kn;
+      VRaw<CH> vn;
+      const bool have = run && kh, first_t = run && first, now = run;
+      bool kh_n = false, int8 = false;
+      int src = 0, b = 0, h = 0, rb = 0, ql = 0;
+      if (run) {
+        src = w.src; b = w.b; h = w.h; rb = w.rb; ql = w.ql;
+        const RowsSource& s = p.src[src];
+        int8 = s.psac_fmt == 1;
         if (have) {
-          const uint4* m4 = cent4 + size_t(min(raw.idx, s.M - 1)) * (D / 8);
+          const uint4* m4 = reinterpret_cast<const uint4*>(s.cent) +
+                            (size_t(h) * s.M + min(k.idx, s.M - 1)) * (D / 8) + part * (CH / 8);
 #pragma unroll
           for (int c = 0; c < CH / 8; ++c) mu[c] = __ldg(m4 + c);
-          if (part == 0) load_psac(s, slot_of((j0 + jj) * kKeys + row), a0, a1);
+          load_value<D, CH>(s, slot, part, vn);
         }
-        Raw<CH> next;
-        const int tn = (j0 + jj + 1) * kKeys + row;
-        const bool have_n = jj + 1 < cnt && tn < len;
-        if (have_n) load_raw<D, CH>(s, slot_of(tn), part, next);
-        uint8_t* kt = smem + Cfg::OFF_K + st * Cfg::K_BYTES;
+        // the next tile
+        ++w.j;
+        first = false;
+        if (w.j >= tiles_of(w.len)) {
+          w.next(p);
+          first = true;
+        }
+        run = w.more();
+        if (run) kh_n = open_tile(kn);
+        if (run && first && pt < N * D / 64) {    // its query rows will be wanted soon
+          const int ri = w.rb * N + pt / (D / 64);
+          if (ri < w.ql * G)
+            prefetch_l2(p.Q + ((size_t(w.b) * p.src[w.src].Nq + ri / G) * p.H_q + w.h * G + ri % G) * D + pt % (D / 64) * 64);
+        }
+      }
+      if (t > 0) {
+        const int st = (t - 1) & 1;
+        if (t > 2) mbar_wait_or_abort(bar + B_VEMPTY + 8 * st, (((t - 1) >> 1) - 1) & 1, p.budget, abort);
         uint8_t* vt = smem + Cfg::OFF_V + st * Cfg::V_BYTES;
-        uint8_t* at = smem + Cfg::OFF_A + st * Cfg::A_BYTES;
-        if (t >= 2) mbar_wait_or_abort(bar + B_KEMPTY + 8 * st, ((t >> 1) - 1) & 1, p.budget, abort);
-        if (have) {
-#pragma unroll
-          for (int lc = 0; lc < CH / 8; ++lc) {
-            const uint32_t sz = raw.ksz[lc / 4];
-            const uint32_t s2 = __byte_perm(sz, 0u, 0x1010u), z2 = __byte_perm(sz, 0u, 0x3232u);
-            const uint32_t add[4] = {hadd2(z2, mu[lc].x), hadd2(z2, mu[lc].y), hadd2(z2, mu[lc].z), hadd2(z2, mu[lc].w)};
-            *reinterpret_cast<uint4*>(kt + sw128_off(row, part * (CH / 8) + lc)) = dequant8(raw.kw[lc >> 1], lc, s2, add);
-          }
-        } else {
-#pragma unroll
-          for (int lc = 0; lc < CH / 8; ++lc)
-            *reinterpret_cast<uint4*>(kt + sw128_off(row, part * (CH / 8) + lc)) = make_uint4(0, 0, 0, 0);
-          a0 = a1 = make_uint4(0, 0, 0, 0);
-        }
-        if (part == 0) {
-          *reinterpret_cast<uint4*>(at + nosw_off(row, 0)) = a0;
-          *reinterpret_cast<uint4*>(at + nosw_off(row, 1)) = a1;
-        }
-        fence_proxy_async();
-        mbar_arrive(bar + B_KFULL + 8 * st);
-        if (t >= 2) mbar_wait_or_abort(bar + B_VEMPTY + 8 * st, ((t >> 1) - 1) & 1, p.budget, abort);
 #pragma unroll
         for (int lc = 0; lc < CH / 8; ++lc) {
           uint4 o = make_uint4(0, 0, 0, 0);
-          if (have) {
-            const uint32_t sz = raw.vsz[lc / 4];
+          if (vh) {
+            const uint32_t sz = v.z[lc / 4];
             const uint32_t s2 = __byte_perm(sz, 0u, 0x1010u), z2 = __byte_perm(sz, 0u, 0x3232u);
             const uint32_t add[4] = {z2, z2, z2, z2};
-            o = dequant8(raw.vw[lc >> 1], lc, s2, add);
+            o = dequant8(v.w[lc >> 1], lc, s2, add);
           }
           *reinterpret_cast<uint4*>(vt + sw128_off(row, part * (CH / 8) + lc)) = o;
         }
         fence_proxy_async();
         mbar_arrive(bar + B_VFULL + 8 * st);
-        raw = next;
-        have = have_n;
       }
-      w.next(p);
+      if (!now) break;
+      const int st = t & 1;
+      if (t >= 2) mbar_wait_or_abort(bar + B_KEMPTY + 8 * st, ((t >> 1) - 1) & 1, p.budget, abort);
+      uint8_t* kt = smem + Cfg::OFF_K + st * Cfg::K_BYTES;
+#pragma unroll
+      for (int lc = 0; lc < CH / 8; ++lc) {
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (have) {
+          const uint32_t sz = k.z[lc / 4];
+          const uint32_t s2 = __byte_perm(sz, 0u, 0x1010u), z2 = __byte_perm(sz, 0u, 0x3232u);
+          const uint32_t add[4] = {hadd2(z2, mu[lc].x), hadd2(z2, mu[lc].y), hadd2(z2, mu[lc].z), hadd2(z2, mu[lc].w)};
+          o = dequant8(k.w[lc >> 1], lc, s2, add);
+        }
+        *reinterpret_cast<uint4*>(kt + sw128_off(row, part * (CH / 8) + lc)) = o;
+      }
+      store_psac(k, int8, have, row, part, smem + Cfg::OFF_A + st * Cfg::A_BYTES);
+      fence_proxy_async();
+      mbar_arrive(bar + B_KFULL + 8 * st);
+      if (first_t) {
+        load_queries(src, b, h, rb, ql);
+        ++seg;
+      }
+      ++t;
+      k = kn;
+      v = vn;
+      vh = have;
+      kh = kh_n;
     }
   } else {
-    // ================= softmax of row group x (thread = key = TMEM lane) =================
-    const int x = warp >> 2, wq = warp & 3, kl = wq * 32 + lane, bid = 2 + x;
+    // ====== softmax of CPT columns (thread = key = TMEM lane) ======
+    const int g = warp >> 2, wq = warp & 3, kl = wq * 32 + lane, bid = 2 + g;
+    const int x = g * CPT / NX, lc0 = g * CPT % NX;          // MMA group, first column within it
     const uint32_t lane_base = uint32_t(wq * 32) << 16;
-    const uint32_t tO = tmem + 2 * N + x * NX + lane_base;
-    float4* tab = reinterpret_cast<float4*>(smem + Cfg::OFF_TAB) + x * (NX / 2);
+    const uint32_t tO = tmem + 2 * N + g * CPT + lane_base;
+    float4* tab = reinterpret_cast<float4*>(smem + Cfg::OFF_TAB) + g * (CPT / 2);
     float* tabf = reinterpret_cast<float*>(tab);
-    float* mrow = reinterpret_cast<float*>(smem + Cfg::OFF_MROW) + x * NX;
-    float* alpha = reinterpret_cast<float*>(smem + Cfg::OFF_ALPHA) + x * NX;
-    int* row_s = reinterpret_cast<int*>(smem + Cfg::OFF_ROW) + x * NX;
-    float* red = reinterpret_cast<float*>(smem + Cfg::OFF_RED) + x * 4 * NX;
+    float* mrow = reinterpret_cast<float*>(smem + Cfg::OFF_MROW) + g * CPT;
+    float* alpha = reinterpret_cast<float*>(smem + Cfg::OFF_ALPHA) + g * CPT;
+    int* row_s = reinterpret_cast<int*>(smem + Cfg::OFF_ROW) + g * CPT;
+    float* red = reinterpret_cast<float*>(smem + Cfg::OFF_RED) + g * 4 * CPT;
     auto wait_pv = [&](int tt) {                // P . V of tile tt is complete
       const int pb = PB == 2 ? (tt & 1) : 0;
       return mbar_wait_or_abort(bar + B_PDONE + 16 * x + 8 * pb, PB == 2 ? (tt >> 1) & 1 : tt & 1, p.budget, abort);
     };
-    float l[NX];
+    float l[CPT];
 #pragma unroll
-    for (int c = 0; c < NX; ++c) l[c] = 0.0f;
+    for (int c = 0; c < CPT; ++c) l[c] = 0.0f;
     bool dead = false;                          // a wait ran out (seen by this thread)
     bool gone = false;                          // ... by the group
     int t = 0, seg = 0;
     for (; w.more(); ++seg) {
       const RowsSource& s = p.src[w.src];
-      const int cnt = w.count(), j0 = w.j, len = w.q.len, h = w.head();
-      const float* scr = reinterpret_cast<const float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + x * NX;
+      const int cnt = w.count(), j0 = w.j, len = w.len, h = w.h;
+      const float* scr = reinterpret_cast<const float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + g * CPT;
       for (int jj = 0; jj < cnt && !gone; ++jj, ++t) {
         const int sbuf = t & 1;
-        const uint32_t tS = tmem + (x * 2 + sbuf) * NX + lane_base;
+        const uint32_t tS = tmem + (x * 2 + sbuf) * NX + lc0 + lane_base;
         dead |= !mbar_wait_or_abort(bar + B_SFULL + 16 * x + 8 * sbuf, (t >> 1) & 1, p.budget, abort);
         fence_after_sync();
         const int k0 = (j0 + jj) * kKeys;
-        const bool valid = k0 + kl < len;
-        bool refresh = true;
-        if (jj == 0) {
-          if (kl < NX) {
-            mrow[kl] = -INFINITY;
-          }
+        const bool valid = k0 + kl < len, full = k0 + kKeys <= len;
+        uint8_t* pt8 = smem + Cfg::OFF_P + (x * PB + (PB == 2 ? sbuf : 0)) * Cfg::P_BYTES;
 #pragma unroll
-          for (int c = 0; c < NX; ++c) l[c] = 0.0f;
-        } else {
-          // does a score pass its row's running maximum by more than the margin?
-          float mx = -INFINITY;
+        for (int c0 = 0; c0 < CPT; c0 += 16) {
+          if (gone) break;
+          uint32_t pw[8];
+          bool checked = jj == 0, refresh = jj == 0;
+#pragma unroll 1
+          for (;;) {
+            if (refresh) {
+              // new maxima for the rows whose scores pass the old ones by more than the margin
+              if (bar_or(bid, 128, dead)) {
+                gone = true;
+                break;
+              }
+              float v[16];
+              tmem_ld16(tS + c0, v);
+              int mine = 0;
 #pragma unroll
-          for (int c0 = 0; c0 < NX; c0 += CW) {
-            float v[CW];
-            tmem_cols<CW>(tS + c0, v);
+              for (int i = 0; i < 16; ++i) {
+                const float sv = valid ? v[i] * scr[c0 + i] : -INFINITY;
+                const int m = __reduce_max_sync(0xffffffffu, f2ord(sv));
+                if (lane == i) mine = m;
+              }
+              if (lane < 16) red[wq * CPT + c0 + lane] = ord2f(mine);
+              // O is rescaled below: P . V of the tile before must be complete
+              if (jj > 0) dead |= !wait_pv(t - 1);
+              fence_after_sync();
+              bar_sync(bid, 128);
+              if (kl < 16) {
+                const int c = c0 + kl;
+                const float tm = fmaxf(fmaxf(red[c], red[CPT + c]), fmaxf(red[2 * CPT + c], red[3 * CPT + c]));
+                // A whole number: every rescaling is by an exact power of two, and
+                // p's rounding does not depend on where the work is cut. Only the
+                // rows that need it: a row's result does not depend on the others.
+                const float mo = jj == 0 ? -INFINITY : mrow[c], mn = tm > mo + (kTrail - kBias) ? ceilf(tm) : mo;
+                alpha[c] = mn == -INFINITY ? 1.0f : ex2(mo - mn);
+                mrow[c] = mn;
+                // s sc - m is one fma, exact to half a step of m: beyond 2^20 (where
+                // a key's fp16 rounding already moves the score by 2^8) the row's
+                // scores are taken at a 2^-k of their size, so that this stays small
+                const float damp =
+                    fabsf(mn) > 0x1p20f && fabsf(mn) < INFINITY ? pow2(-max(exp_above(fabsf(mn)) - 21, 0)) : 1.0f;
+                tabf[(c >> 1) * 4 + (c & 1)] = scr[c] * damp;
+                tabf[(c >> 1) * 4 + 2 + (c & 1)] = mn == -INFINITY ? 0.0f : kBias - mn * damp;
+              }
+              bar_sync(bid, 128);
+              if (jj > 0) {
 #pragma unroll
-            for (int i = 0; i < CW; i += 2) {
+                for (int i = 0; i < 16; ++i) l[c0 + i] *= alpha[c0 + i];
+                uint32_t o[16];
+                tmem_ld16(tO + c0, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(v[i] * alpha[c0 + i]);
+                tmem_st16(tO + c0, o);
+                tmem_wait_st();
+              }
+            }
+            float v[16], mx = -INFINITY;
+            tmem_ld16(tS + c0, v);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
               const float4 k = tab[(c0 + i) >> 1];
               const float2 xx = up2(ffma2(pk2(v[i], v[i + 1]), pk2(k.x, k.y), pk2(k.z, k.w)));
               mx = fmax3(mx, xx.x, xx.y);
+              pw[i / 2] = pack_f16(ex2(xx.x), ex2(xx.y));
             }
+            if (checked) break;
+            checked = true;
+            refresh = bar_or(bid, 128, (valid && mx > kTrail) || dead);
+            if (!refresh) break;
           }
-          refresh = bar_or(bid, 128, (valid && mx > kTrail) || dead);
-        }
-        if (refresh) {
-          if (bar_or(bid, 128, dead)) { gone = true; break; }
+          if (gone) break;
+          if (!full) {
 #pragma unroll
-          for (int c0 = 0; c0 < NX; c0 += CW) {
-            float v[CW];
-            tmem_cols<CW>(tS + c0, v);
-            int mine = 0;
-#pragma unroll
-            for (int i = 0; i < CW; ++i) {
-              const float sv = valid ? v[i] * scr[c0 + i] : -INFINITY;
-              const int m = __reduce_max_sync(0xffffffffu, f2ord(sv));
-              if (lane == i) mine = m;
-            }
-            if (lane < CW) red[wq * NX + c0 + lane] = ord2f(mine);
+            for (int i = 0; i < 8; ++i) pw[i] = valid ? pw[i] : 0u;
           }
-          // O is rescaled below: P . V of the tile before must be complete
-          if (jj > 0) dead |= !wait_pv(t - 1);
-          fence_after_sync();
-          bar_sync(bid, 128);
-          if (kl < NX) {
-            const float tm = fmaxf(fmaxf(red[kl], red[NX + kl]), fmaxf(red[2 * NX + kl], red[3 * NX + kl]));
-            // A whole number: every rescaling is by an exact power of two, and
-            // p's rounding does not depend on where the work is cut. Only the
-            // rows that need it: a row's result does not depend on the others.
-            const float mo = mrow[kl], mn = tm > mo + (kTrail - kBias) ? ceilf(tm) : mo;
-            alpha[kl] = mn == -INFINITY ? 1.0f : ex2(mo - mn);
-            mrow[kl] = mn;
-            // s sc - m is one fma, exact to half a step of m: beyond 2^20 (where
-            // a key's fp16 rounding already moves the score by 2^8) the row's
-            // scores are taken at a 2^-k of their size, so that this stays small
-            int e = 0;
-            if (fabsf(mn) > 0x1p20f && fabsf(mn) < INFINITY) frexpf(mn, &e);
-            const float damp = ldexpf(1.0f, -max(e - 21, 0));
-            tabf[(kl >> 1) * 4 + (kl & 1)] = scr[kl] * damp;
-            tabf[(kl >> 1) * 4 + 2 + (kl & 1)] = mn == -INFINITY ? 0.0f : kBias - mn * damp;
-          }
-          bar_sync(bid, 128);
-          if (jj > 0) {
-#pragma unroll
-            for (int c = 0; c < NX; ++c) l[c] *= alpha[c];
-#pragma unroll
-            for (int c0 = 0; c0 < NX; c0 += 16) {
-              float v[16];
-              uint32_t o[16];
-              tmem_ld16(tO + c0, v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(v[i] * alpha[c0 + i]);
-              tmem_st16(tO + c0, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        // ---- probabilities into the P operand, once its buffer is free
-        if (t >= PB) dead |= !wait_pv(t - PB);
-        uint8_t* pt8 = smem + Cfg::OFF_P + (x * PB + (PB == 2 ? sbuf : 0)) * Cfg::P_BYTES;
-        const bool full = k0 + kKeys <= len;
-#pragma unroll
-        for (int c0 = 0; c0 < NX; c0 += CW) {
-          float v[CW];
-          tmem_cols<CW>(tS + c0, v);
-          if (c0 + CW == NX) {                    // the scores are in registers: the buffer may be rewritten
+          if (c0 + 16 == CPT) {                   // all scores are read: the buffer may be rewritten
             fence_before_sync();
             mbar_arrive(bar + B_SFREE + 16 * x + 8 * sbuf);
           }
-          uint32_t pw2[CW / 2];
+          // the sums of what enters P . V (the unit's first tile starts them)
 #pragma unroll
-          for (int i = 0; i < CW; i += 2) {
-            const float4 k = tab[(c0 + i) >> 1];
-            const float2 xx = up2(ffma2(pk2(v[i], v[i + 1]), pk2(k.x, k.y), pk2(k.z, k.w)));
-            float p0 = ex2(xx.x), p1 = ex2(xx.y);
-            if (!full) {
-              p0 = valid ? p0 : 0.0f;
-              p1 = valid ? p1 : 0.0f;
-            }
-            l[c0 + i] += p0;
-            l[c0 + i + 1] += p1;
-            pw2[i / 2] = pack_f16(p0, p1);
+          for (int i = 0; i < 8; ++i) {
+            if (jj == 0) l[c0 + 2 * i] = l[c0 + 2 * i + 1] = 0.0f;
+            add_f16x2(l[c0 + 2 * i], l[c0 + 2 * i + 1], pw[i]);
           }
+          if (c0 == 0 && t >= PB) dead |= !wait_pv(t - PB);    // the buffer is free
           if constexpr (NX == 64) {
             // rows along the operand's contiguous dimension: [key][64 rows], swizzled
-#pragma unroll
-            for (int i = 0; i < CW / 8; ++i)
-              *reinterpret_cast<uint4*>(pt8 + kl * 128 + (((c0 / 8 + i) ^ (kl & 7)) << 4)) =
-                  make_uint4(pw2[4 * i], pw2[4 * i + 1], pw2[4 * i + 2], pw2[4 * i + 3]);
+            const int ck = (lc0 + c0) / 8;
+            *reinterpret_cast<uint4*>(pt8 + kl * 128 + ((ck ^ (kl & 7)) << 4)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            *reinterpret_cast<uint4*>(pt8 + kl * 128 + (((ck + 1) ^ (kl & 7)) << 4)) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
           } else {
             // keys along the contiguous dimension: [2][row][64 keys], swizzled
 #pragma unroll
-            for (int i = 0; i < CW; ++i) {
-              const int rr = c0 + i;
+            for (int i = 0; i < 16; ++i) {
+              const int rr = lc0 + c0 + i;
               *reinterpret_cast<uint16_t*>(pt8 + (kl >> 6) * NX * 128 + rr * 128 + ((((kl & 63) >> 3) ^ (rr & 7)) << 4) +
-                                           (kl & 7) * 2) = uint16_t((i & 1) ? pw2[i / 2] >> 16 : pw2[i / 2] & 0xffffu);
+                                           (kl & 7) * 2) = uint16_t((i & 1) ? pw[i / 2] >> 16 : pw[i / 2] & 0xffffu);
             }
           }
         }
+        if (gone) break;
         fence_proxy_async();
         fence_before_sync();
         mbar_arrive(bar + B_PFULL + 16 * x + 8 * (PB == 2 ? sbuf : 0));
@@ -894,17 +924,14 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
         fence_after_sync();
         gone = bar_or(bid, 128, dead);
       }
-      warp_colsum<NX>(l, lane);
-      if (NX >= 32 || lane < NX) {
-#pragma unroll
-        for (int c = 0; c < (NX + 31) / 32; ++c) red[wq * NX + c * 32 + lane] = l[c];
-      }
+      warp_colsum<CPT>(l, lane);
+      if (lane < CPT) red[wq * CPT + lane] = l[0];
       bar_sync(bid, 128);
-      const bool whole = j0 == 0 && cnt == w.q.nb;
+      const bool whole = j0 == 0 && cnt == tiles_of(len);
       const int slot = j0 > 0 ? 0 : 1;
-      const int r0 = w.block() * N + x * NX, live = min(NX, w.q.ql * G - r0);
-      if (kl < NX) {
-        float lt = (red[kl] + red[NX + kl]) + (red[2 * NX + kl] + red[3 * NX + kl]);
+      const int r0 = w.rb * N + g * CPT, live = min(CPT, w.ql * G - r0);
+      if (kl < CPT) {
+        float lt = (red[kl] + red[CPT + kl]) + (red[2 * CPT + kl] + red[3 * CPT + kl]);
         float m = mrow[kl];
         if (gone) {
           lt = 1.0f;
@@ -915,13 +942,13 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
           // row of (sequence, query, head) in Q and out
           const int ri = r0 + kl, row = (w.b * s.Nq + ri / G) * p.H_q + h * G + ri % G;
           row_s[kl] = row;
-          if (!whole) p.part_ml[(size_t(blockIdx.x) * 2 + slot) * N + x * NX + kl] = make_float2(m, lt);
+          if (!whole) p.part_ml[(size_t(blockIdx.x) * 2 + slot) * N + g * CPT + kl] = make_float2(m, lt);
           else if (!p.out) p.dir_ml[size_t(w.src) * p.dir_rows + row] = make_float2(m, lt);
         }
       }
       bar_sync(bid, 128);
 #pragma unroll 1
-      for (int c0 = 0; c0 < NX; c0 += 16) {
+      for (int c0 = 0; c0 < CPT; c0 += 16) {
         if (c0 >= live) break;
         float v[16];
         if (!gone) {
@@ -936,7 +963,7 @@ __global__ void __launch_bounds__(RCfg<D, NX, X>::kThreads, 1) rows_attn_kernel(
             const int c = c0 + i;
             if (c >= live) break;
             if (!whole) {
-              p.part_o[((size_t(blockIdx.x) * 2 + slot) * N + x * NX + c) * D + kl] = v[i];
+              p.part_o[((size_t(blockIdx.x) * 2 + slot) * N + g * CPT + c) * D + kl] = v[i];
             } else if (!p.out) {
               p.dir_o[(size_t(w.src) * p.dir_rows + row_s[c]) * D + kl] = v[i];
             } else {
@@ -1039,16 +1066,16 @@ __global__ void __launch_bounds__(256) rows_merge_cut(const __grid_constant__ Ro
   const int4 at = p.cta[c];
   if (at.w == 0) return;                          // no unit is cut here
   const int G = p.H_q / p.H_kv;
-  const SeqShape q = seq_shape<N>(p.src[0], at.y, G);
+  const int ql = seq_queries(p.src[0], at.y), RB = blocks_of<N>(ql, G);
   const long long u = lo - at.w;                  // position of the unit's first tile
-  const int c0 = part_of(u, T, C), c1 = part_of(u + q.nb - 1, T, C);
+  const int c0 = part_of(u, T, C), c1 = part_of(u + tiles_of(seq_len(p.src[0], at.y)) - 1, T, C);
   if (part_begin(T, c0 + 1, C) != lo) return;     // an earlier border of the same unit
   const int row = blockIdx.y * 8 + warp;
-  const int ri = (at.z % q.RB) * N + row;
-  if (ri >= q.ql * G) return;
+  const int ri = (at.z % RB) * N + row;
+  if (ri >= ql * G) return;
   float m, l, o[D / 32];
   merge_pieces<D>(p.part_o, p.part_ml, N, row, c0, c1, T, C, lane, m, l, o);
-  const size_t gr = (size_t(at.y) * p.src[0].Nq + ri / G) * p.H_q + (at.z / q.RB) * G + ri % G;
+  const size_t gr = (size_t(at.y) * p.src[0].Nq + ri / G) * p.H_q + (at.z / RB) * G + ri % G;
   store_row<D>(p.out, p.out_dtype, gr, lane, l, o);
 }
 
@@ -1067,11 +1094,11 @@ __global__ void __launch_bounds__(256) rows_merge_shared(const __grid_constant__
   for (int s = 0; s < 2; ++s) {
     const RowsSource& src = p.src[s];
     const int seq = int(gr / p.H_q), b = seq / src.Nq, i = seq % src.Nq;
-    const SeqShape q = seq_shape<N>(src, b, G);
+    const int nb = tiles_of(seq_len(src, b)), RB = blocks_of<N>(src.Nq, G);
     const int ri = i * G + g;
     const long long u = p.base[(s ? p.src[0].B : 0) + b] +
-                        (static_cast<long long>(h) * q.RB + ri / N) * (q.nb + kLead) + kLead;
-    const int c0 = part_of(u, T, C), c1 = part_of(u + q.nb - 1, T, C);
+                        (static_cast<long long>(h) * RB + ri / N) * (nb + kLead) + kLead;
+    const int c0 = part_of(u, T, C), c1 = part_of(u + nb - 1, T, C);
     if (c0 == c1) {
       const float2 ml = p.dir_ml[size_t(s) * p.dir_rows + gr];
       m[s] = ml.x;
@@ -1139,10 +1166,10 @@ RowsPlan plan_rows(const RowsArgs& a) {
   return pl;
 }
 
-template <int D, int NX, int X>
+template <int D, int N>
 cudaError_t launch_cfg(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) {
-  using Cfg = RCfg<D, NX, X>;
-  auto kern = rows_attn_kernel<D, NX, X>;
+  using Cfg = RCfg<D, N>;
+  auto kern = rows_attn_kernel<D, N>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg::SMEM));
   if (e != cudaSuccess) return e;
   RowsParams q = p;
@@ -1165,10 +1192,10 @@ cudaError_t launch_cfg(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) 
 template <int D>
 cudaError_t launch_d(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) {
   switch (pl.N) {
-    case 16: return launch_cfg<D, 16, 1>(p, pl, s);
-    case 32: return launch_cfg<D, 32, 1>(p, pl, s);
-    case 64: return launch_cfg<D, 64, 1>(p, pl, s);
-    default: return launch_cfg<D, 64, 2>(p, pl, s);
+    case 16: return launch_cfg<D, 16>(p, pl, s);
+    case 32: return launch_cfg<D, 32>(p, pl, s);
+    case 64: return launch_cfg<D, 64>(p, pl, s);
+    default: return launch_cfg<D, 128>(p, pl, s);
   }
 }
 
