@@ -90,6 +90,9 @@ struct RowsSource {
 struct RowsParams {
   RowsSource src[2];
   int nsrc, H_kv, H_q;
+  uint32_t g_inv;           // ceil(2^32 / G), G = H_q / H_kv > 1 (G = 1: 0)
+  // row / G, for row * G < 2^32
+  __device__ int per_head(int row) const { return g_inv ? int(__umulhi(uint32_t(row), g_inv)) : row; }
   const uint16_t* Q;        // bf16 [rows of (b, i)][H_q][D]
   void* out;                // null: whole units go to dir_o / dir_ml
   int out_dtype;
@@ -118,18 +121,26 @@ struct RCfg {
   // producers: 4 threads per key (16 warps hide the loads' latency); at 128
   // rows, where the softmax has 16 warps, 2
   static constexpr int TPR = N == 128 ? 2 : 4, PW = kKeys * TPR / 32;
-  static constexpr int kMmaWarp = SW + PW, kThreads = 32 * (SW + PW + 1);
+  static constexpr int kMmaWarp = SW + PW, kLoadWarp = kMmaWarp + 1, kThreads = 32 * (SW + PW + 2);
   static constexpr int CH = D / TPR;                 // channels per producer thread
   static constexpr int PB = X == 1 ? 2 : 1;          // P buffers per MMA group
+  static constexpr int VS = N == 128 ? 1 : 2;        // value stages (128 rows: what shared memory leaves)
+  static constexpr int RS = N <= 32 ? 3 : 1;         // stages of packed tiles
+  // packed tile: codes of keys and values, scale and zero words, ids, PSAC
+  // (fp16, or int8 codes and from RAW_PSC on the tokens' scales)
+  static constexpr int RAW_VC = kKeys * D / 4, RAW_KZ = 2 * RAW_VC, RAW_VZ = RAW_KZ + kKeys * D / 8;
+  static constexpr int RAW_IX = RAW_VZ + kKeys * D / 8, RAW_PS = RAW_IX + 2 * kKeys, RAW_PSC = RAW_PS + kKeys * 16;
+  static constexpr int RAW_BYTES = RAW_PS + kKeys * 32;
   static constexpr int Q_BYTES = NX * D * 2, U_BYTES = NX * 32, K_BYTES = kKeys * D * 2, A_BYTES = kKeys * 32;
   static constexpr int V_BYTES = kKeys * 256;        // 128 channels (zero above D)
   static constexpr int P_BYTES = NX * 256;
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_V = OFF_K + kStages * K_BYTES;
-  static constexpr uint32_t OFF_Q = OFF_V + kStages * V_BYTES;
+  static constexpr uint32_t OFF_Q = OFF_V + VS * V_BYTES;
   static constexpr uint32_t OFF_P = OFF_Q + X * Q_BYTES;
   static constexpr uint32_t OFF_A = OFF_P + X * PB * P_BYTES;
-  static constexpr uint32_t OFF_U = OFF_A + kStages * A_BYTES;
+  static constexpr uint32_t OFF_RAW = OFF_A + kStages * A_BYTES;
+  static constexpr uint32_t OFF_U = OFF_RAW + RS * RAW_BYTES;
   static constexpr uint32_t OFF_FRAG = OFF_U + X * U_BYTES;             // P fragments [D/16][2][2][32] uint2
   static constexpr uint32_t OFF_SCR = OFF_FRAG + D / 16 * 2 * 2 * 32 * 8;   // row scales, ring of 4 units
   static constexpr uint32_t OFF_QE = OFF_SCR + 4 * N * 4;               // row exponents of the unit being loaded
@@ -139,7 +150,7 @@ struct RCfg {
   static constexpr uint32_t OFF_ROW = OFF_ALPHA + N * 4;                // row of Q and out per column
   static constexpr uint32_t OFF_RED = OFF_ROW + N * 4;                  // [SG][4 warps][CPT]
   static constexpr uint32_t OFF_BAR = OFF_RED + 4 * N * 4;
-  static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
+  static constexpr uint32_t SMEM = OFF_BAR + 288 + 1024;
   static constexpr uint32_t kTmemUsed = 3 * N;
   static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   // Q and Khat K-major; Vhat by channels; P by rows (NX = 64) or by keys
@@ -151,7 +162,7 @@ struct RCfg {
 // barrier slots (bytes from OFF_BAR)
 constexpr uint32_t B_KFULL = 0, B_KEMPTY = 16, B_VFULL = 32, B_VEMPTY = 48, B_SFULL = 64, B_SFREE = 96,
                    B_PFULL = 128, B_PDONE = 160, B_QFULL = 192, B_QEMPTY = 200, B_FINAL = 208, B_NEVER = 216,
-                   B_TMEM = 224, B_ABORT = 228;
+                   B_TMEM = 224, B_ABORT = 228, B_RFULL = 232, B_REMPTY = 256;
 
 // order-preserving map of floats to signed integers, and back
 __device__ __forceinline__ int f2ord(float x) {
@@ -191,7 +202,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // e with |x| < 2^e (finite x; -126 at least), and 2^e
 __device__ __forceinline__ int exp_above(float x) { return int((__float_as_uint(x) >> 23) & 0xffu) - 126; }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
@@ -313,86 +323,21 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
 // producers
 // ---------------------------------------------------------------------------
 
-// Packed fields of CH channels of a cached token, channels part * CH ..; of
-// its key also the centre's id and 16 / TPR PSAC coefficients (fp16, or int8
-// codes and the token's scale in the last word).
-template <int CH, int TPR>
-struct KRaw {
-  static constexpr int W = CH / 16, Z = CH >= 64 ? 2 : 1, CP = 16 / TPR;
-  uint32_t w[W], z[Z], ps[CP / 2];
-  int idx;
-};
-template <int CH>
-struct VRaw {
-  static constexpr int W = CH / 16, Z = CH >= 64 ? 2 : 1;
-  uint32_t w[W], z[Z];
-};
-
+// N consecutive 32-bit words of shared memory
 template <int W>
-__device__ __forceinline__ void load_words(const void* src, uint32_t (&w)[W]) {
+__device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[W]) {
   if constexpr (W == 4) {
-    const uint4 v = *static_cast<const uint4*>(src);
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   } else if constexpr (W == 2) {
-    const uint2 v = *static_cast<const uint2*>(src);
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
     w[0] = v.x; w[1] = v.y;
   } else {
-    w[0] = *static_cast<const uint32_t*>(src);
+    w[0] = *reinterpret_cast<const uint32_t*>(src);
   }
 }
-template <int D, int CH, int Z>
-__device__ __forceinline__ void load_sz(const uint32_t* sz, size_t slot, int gshift, int part, uint32_t (&z)[Z]) {
-  const uint32_t* row = sz + slot * (D >> gshift);
-#pragma unroll
-  for (int i = 0; i < Z; ++i) z[i] = row[(part * CH + 32 * i) >> gshift];
-}
 
-template <int D, int CH, int TPR>
-__device__ __forceinline__ void load_key(const RowsSource& s, size_t slot, int part, KRaw<CH, TPR>& r) {
-  constexpr int CP = KRaw<CH, TPR>::CP;
-  r.idx = (s.M <= 256) ? int(static_cast<const uint8_t*>(s.cidx)[slot]) : int(static_cast<const uint16_t*>(s.cidx)[slot]);
-  load_words(s.k_code + slot * (D / 16) + part * (CH / 16), r.w);
-  load_sz<D, CH>(s.k_sz, slot, s.gshift, part, r.z);
-#pragma unroll
-  for (int i = 0; i < CP / 2; ++i) r.ps[i] = 0u;
-  if (part * CP < s.r) {
-    if (s.psac_fmt == 1) {
-      uint32_t q[CP / 4];
-      load_words(reinterpret_cast<const int8_t*>(s.psac) + slot * s.r + part * CP, q);
-#pragma unroll
-      for (int i = 0; i < CP / 4; ++i) r.ps[i] = q[i];
-      r.ps[CP / 2 - 1] = s.psac_scale[slot];
-    } else {
-      load_words(s.psac + slot * s.r + part * CP, r.ps);
-    }
-  }
-}
-template <int D, int CH>
-__device__ __forceinline__ void load_value(const RowsSource& s, size_t slot, int part, VRaw<CH>& r) {
-  load_words(s.v_code + slot * (D / 16) + part * (CH / 16), r.w);
-  load_sz<D, CH>(s.v_sz, slot, s.gshift, part, r.z);
-}
-
-// the part's PSAC coefficients as fp16 into the operand row (int8: fp16(code * scale))
-template <int CH, int TPR>
-__device__ __forceinline__ void store_psac(const KRaw<CH, TPR>& r, bool int8, bool have, int row, int part, uint8_t* tile) {
-  constexpr int CP = KRaw<CH, TPR>::CP;
-  uint32_t a[CP / 2];
-#pragma unroll
-  for (int i = 0; i < CP / 2; ++i) a[i] = have ? r.ps[i] : 0u;
-  if (int8 && have) {
-    const float sc = __half2float(__ushort_as_half(uint16_t(r.ps[CP / 2 - 1])));
-#pragma unroll
-    for (int i = 0; i < CP / 2; ++i) {
-      const uint32_t two = (r.ps[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-      a[i] = pack_f16(float(int8_t(two & 0xff)) * sc, float(int8_t(two >> 8)) * sc);
-    }
-  }
-  uint8_t* dst = tile + nosw_off(row, part * CP / 8) + (part * CP % 8) * 2;
-  if constexpr (CP == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
-  else *reinterpret_cast<uint2*>(dst) = make_uint2(a[0], a[1]);
-}
-
+// eight channels: codes lc of a code word times s2 plus add, in fp16 pairs
 __device__ __forceinline__ uint4 dequant8(uint32_t word, int lc, uint32_t s2, const uint32_t (&add)[4]) {
   const uint32_t x = field_both(word, lc), x8 = x >> 8;
   uint32_t o[4];
@@ -453,11 +398,15 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       mbar_init(bar + B_PFULL + 8 * i, SW * 32 / X);
       mbar_init(bar + B_PDONE + 8 * i, 1);
     }
+    for (int i = 0; i < Cfg::RS; ++i) {
+      mbar_init(bar + B_RFULL + 8 * i, 1);
+      mbar_init(bar + B_REMPTY + 8 * i, PW);
+    }
     mbar_init(bar + B_QFULL, PW * 32);
     mbar_init(bar + B_QEMPTY, 1);
     mbar_init(bar + B_FINAL, 1);
     mbar_init(bar + B_NEVER, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_init_fence();
     *abort = 0;
   }
   if (warp == Cfg::kMmaWarp) tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
@@ -471,8 +420,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     }
   }
   if constexpr (D < 128) {
-    // the channels above D of both value stages stay zero
-    for (int i = tid; i < kStages * kKeys * 8; i += Cfg::kThreads)
+    // the channels above D of the value stages stay zero
+    for (int i = tid; i < Cfg::VS * kKeys * 8; i += Cfg::kThreads)
       *reinterpret_cast<uint4*>(smem + Cfg::OFF_V + (i / (kKeys * 8)) * Cfg::V_BYTES + 16384 + (i % (kKeys * 8)) * 16) =
           make_uint4(0, 0, 0, 0);
     fence_proxy_async();
@@ -496,8 +445,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     int t = 0, seg = 0;
     // P . V of tile tt (the first of its unit's part starts the sums afresh)
     auto issue_pv = [&](int tt, bool first) __attribute__((always_inline)) -> bool {
-      const int s = tt & 1;
-      if (!mbar_wait_or_abort(bar + B_VFULL + 8 * s, (tt >> 1) & 1, p.budget, abort)) return false;
+      const int s = tt % Cfg::VS;
+      if (!mbar_wait_or_abort(bar + B_VFULL + 8 * s, (tt / Cfg::VS) & 1, p.budget, abort)) return false;
       for (int x = 0; x < X; ++x) {
         const int pb = PB == 2 ? (tt & 1) : 0;
         const uint32_t par = PB == 2 ? (tt >> 1) & 1 : tt & 1;
@@ -562,6 +511,46 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       w.next(p);
     }
     if (ok && pend) issue_pv(t - 1, pend_first);
+  } else if (warp == Cfg::kLoadWarp) {
+    // ================= packed tiles (one thread, bulk copies) =================
+    if (lane == 0) {
+      int t = 0;
+      for (; w.more(); w.next(p)) {
+        const RowsSource& s = p.src[w.src];
+        const int cnt = w.count(), sz = (D >> s.gshift) * 4, id = s.M <= 256 ? 1 : 2;
+        const int ps = s.psac_fmt == 1 ? s.r : 2 * s.r, psc = s.psac_fmt == 1 && s.r ? 2 : 0;
+        bool out = false;
+        for (int jj = 0; jj < cnt; ++jj, ++t) {
+          const int st = t % Cfg::RS, tok = (w.j + jj) * kKeys;
+          if (t >= Cfg::RS && !mbar_wait_or_abort(bar + B_REMPTY + 8 * st, (t / Cfg::RS - 1) & 1, p.budget, abort)) {
+            out = true;
+            break;
+          }
+          const uint32_t full = bar + B_RFULL + 8 * st, dst = sb + Cfg::OFF_RAW + st * Cfg::RAW_BYTES;
+          // whole runs of 16 tokens (16-byte copies), within the capacity, which is a multiple of 16;
+          // a tile never leaves its page
+          const int n = (min(kKeys, w.len - tok) + 15) & ~15;
+          if (n <= 0) {                           // an empty sequence's masked tile
+            mbar_arrive(full);
+            continue;
+          }
+          const size_t slot = cache_slot(s.table, s.page, p.H_kv, s.cap, w.b, w.h, tok);
+          mbar_arrive_expect_tx(full, uint32_t(n) * uint32_t(D / 2 + 2 * sz + id + ps + psc));
+          bulk_g2s(dst, s.k_code + slot * (D / 16), n * (D / 4), full);
+          bulk_g2s(dst + Cfg::RAW_KZ, reinterpret_cast<const uint8_t*>(s.k_sz) + slot * sz, n * sz, full);
+          bulk_g2s(dst + Cfg::RAW_IX, static_cast<const uint8_t*>(s.cidx) + slot * id, n * id, full);
+          if (ps) bulk_g2s(dst + Cfg::RAW_PS, reinterpret_cast<const uint8_t*>(s.psac) + slot * ps, n * ps, full);
+          if (psc) bulk_g2s(dst + Cfg::RAW_PSC, s.psac_scale + slot, n * 2, full);
+          bulk_g2s(dst + Cfg::RAW_VC, s.v_code + slot * (D / 16), n * (D / 4), full);
+          bulk_g2s(dst + Cfg::RAW_VZ, reinterpret_cast<const uint8_t*>(s.v_sz) + slot * sz, n * sz, full);
+        }
+        if (out) break;
+      }
+      // copies still in flight land before the block ends (after an abort the
+      // producers no longer wait for them)
+      for (int i = max(0, t - Cfg::RS); i < t; ++i)
+        mbar_wait(bar + B_RFULL + 8 * (i % Cfg::RS), (i / Cfg::RS) & 1, p.budget);
+    }
   } else if (warp >= SW) {
     // ================= producers =================
     // lanes 8q..8q+7 of a warp take 8 consecutive keys and one part of their
@@ -575,10 +564,23 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     // The query rows of a unit, warp g rows 16 g .. 16 g + 15: copied raw, their
     // product with the basis (bf16 query, exact; P as two bf16 numbers, 2^-16),
     // then both scaled by 2^e per row, max(|q|, |u|) 2^e < 2^15, to fp16.
-    auto load_queries = [&](int src, int b, int h, int rb, int ql) __attribute__((always_inline)) {
-      const RowsSource& s = p.src[src];
-      if (s.r > 0 && (src != frag_src || h != frag_h)) {
-        const float* Ph = s.P + size_t(h) * D * s.r;
+    auto load_queries = [&]() __attribute__((always_inline)) {
+      const RowsSource& s = p.src[w.src];
+      constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;       // lanes per row, rows per step, steps
+      const int c = lane % LPR, x = pw * 16 / NX, r0 = pw * 16 % NX;
+      auto q_off = [&](int rx, int ck) { return (ck >> 3) * NX * 128 + rx * 128 + (((ck & 7) ^ (rx & 7)) << 4); };
+      if (pw < N / 16) {
+        if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+          const int rx = r0 + k * RPI + lane / LPR, ri = w.rb * N + x * NX + rx, i = p.per_head(ri);
+          const bool in = ri < w.ql * G;
+          const size_t gr = in ? (size_t(w.b) * s.Nq + i) * p.H_q + w.h * G + (ri - i * G) : 0;
+          copy16(sb + Cfg::OFF_Q + x * Cfg::Q_BYTES + q_off(rx, c), p.Q + gr * D + c * 8, in);
+        }
+      }
+      if (s.r > 0 && (w.src != frag_src || w.h != frag_h)) {
+        const float* Ph = s.P + size_t(w.h) * D * s.r;
         bar_sync(1, PW * 32);                     // the previous fragments are read
         for (int i = pt; i < D / 16 * 2 * 32; i += PW * 32) {
           const int l = i & 31, nt = (i >> 5) & 1, ks = i >> 6;
@@ -594,22 +596,11 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
           frag[((ks * 2 + nt) * 2 + 1) * 32 + l] = make_uint2(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]));
         }
         bar_sync(1, PW * 32);
-        frag_src = src;
-        frag_h = h;
+        frag_src = w.src;
+        frag_h = w.h;
       }
       if (pw < N / 16) {
-        constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;     // lanes per row, rows per step, steps
-        const int c = lane % LPR, x = pw * 16 / NX, r0 = pw * 16 % NX;
         uint8_t* qt = smem + Cfg::OFF_Q + x * Cfg::Q_BYTES;
-        auto q_off = [&](int rx, int ck) { return (ck >> 3) * NX * 128 + rx * 128 + (((ck & 7) ^ (rx & 7)) << 4); };
-        if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-          const int rx = r0 + k * RPI + lane / LPR, ri = rb * N + x * NX + rx;
-          const bool in = ri < ql * G;
-          const size_t gr = in ? (size_t(b) * s.Nq + ri / G) * p.H_q + h * G + ri % G : 0;
-          copy16(sb + Cfg::OFF_Q + x * Cfg::Q_BYTES + q_off(rx, c), p.Q + gr * D + c * 8, in);
-        }
         float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + pw * 16;
         int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE) + pw * 16;
         copy_wait();
@@ -681,103 +672,104 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       mbar_arrive(bar + B_QFULL);
     };
 
-    // Tile by tile: the centre rows of tile t (their ids arrived with the
-    // packed key a tile ago) and the packed fields of the next are requested,
-    // the values of tile t - 1 are written meanwhile, then the keys of tile t.
-    KRaw<CH, TPR> k;
-    VRaw<CH> v;
-    size_t slot = 0;
-    bool kh = false, vh = false;                // the thread's token of tile t (t - 1) exists
-    auto open_tile = [&](KRaw<CH, TPR>& r) __attribute__((always_inline)) {
-      const RowsSource& s = p.src[w.src];
-      const int tok = w.j * kKeys + row;
-      if (tok >= w.len) return false;
-      slot = cache_slot(s.table, s.page, p.H_kv, s.cap, w.b, w.h, tok);
-      load_key<D, CH, TPR>(s, slot, part, r);
-      return true;
-    };
-    bool run = w.more(), first = true;
-    if (run) kh = open_tile(k);
-#pragma unroll 1
-    while (run || t > 0) {                       // one round more than tiles: the last tile's values
-      uint4 mu[CH / 8];
-      KRaw<CH, TPR> kn;
-      VRaw<CH> vn;
-      const bool have = run && kh, first_t = run && first, now = run;
-      bool kh_n = false, int8 = false;
-      int src = 0, b = 0, h = 0, rb = 0, ql = 0;
-      if (run) {
-        src = w.src; b = w.b; h = w.h; rb = w.rb; ql = w.ql;
-        const RowsSource& s = p.src[src];
-        int8 = s.psac_fmt == 1;
-        if (have) {
-          const uint4* m4 = reinterpret_cast<const uint4*>(s.cent) +
-                            (size_t(h) * s.M + min(k.idx, s.M - 1)) * (D / 8) + part * (CH / 8);
-#pragma unroll
-          for (int c = 0; c < CH / 8; ++c) mu[c] = __ldg(m4 + c);
-          load_value<D, CH>(s, slot, part, vn);
-        }
-        // the next tile
-        ++w.j;
-        first = false;
-        if (w.j >= tiles_of(w.len)) {
-          w.next(p);
-          first = true;
-        }
-        run = w.more();
-        if (run) kh_n = open_tile(kn);
-        if (run && first && pt < N * D / 64) {    // its query rows will be wanted soon
-          const int ri = w.rb * N + pt / (D / 64);
-          if (ri < w.ql * G)
-            prefetch_l2(p.Q + ((size_t(w.b) * p.src[w.src].Nq + ri / G) * p.H_q + w.h * G + ri % G) * D + pt % (D / 64) * 64);
-        }
-      }
-      if (t > 0) {
-        const int st = (t - 1) & 1;
-        if (t > 2) mbar_wait_or_abort(bar + B_VEMPTY + 8 * st, (((t - 1) >> 1) - 1) & 1, p.budget, abort);
-        uint8_t* vt = smem + Cfg::OFF_V + st * Cfg::V_BYTES;
-#pragma unroll
-        for (int lc = 0; lc < CH / 8; ++lc) {
-          uint4 o = make_uint4(0, 0, 0, 0);
-          if (vh) {
-            const uint32_t sz = v.z[lc / 4];
-            const uint32_t s2 = __byte_perm(sz, 0u, 0x1010u), z2 = __byte_perm(sz, 0u, 0x3232u);
-            const uint32_t add[4] = {z2, z2, z2, z2};
-            o = dequant8(v.w[lc >> 1], lc, s2, add);
-          }
-          *reinterpret_cast<uint4*>(vt + sw128_off(row, part * (CH / 8) + lc)) = o;
-        }
-        fence_proxy_async();
-        mbar_arrive(bar + B_VFULL + 8 * st);
-      }
-      if (!now) break;
-      const int st = t & 1;
-      if (t >= 2) mbar_wait_or_abort(bar + B_KEMPTY + 8 * st, ((t >> 1) - 1) & 1, p.budget, abort);
-      uint8_t* kt = smem + Cfg::OFF_K + st * Cfg::K_BYTES;
+    // Tile by tile: the packed fields move to registers, the centre rows of the
+    // tile's ids are requested, the values of tile t - 1 are written meanwhile,
+    // then the keys of tile t.
+    uint32_t vw[CH / 16], vz[CH >= 64 ? 2 : 1];
+    bool vh = false;                             // the thread's token of tile t - 1 exists
+    auto write_values = [&](int tt) __attribute__((always_inline)) {
+      const int st = tt % Cfg::VS;
+      if (tt >= Cfg::VS) mbar_wait_or_abort(bar + B_VEMPTY + 8 * st, (tt / Cfg::VS - 1) & 1, p.budget, abort);
+      uint8_t* vt = smem + Cfg::OFF_V + st * Cfg::V_BYTES;
 #pragma unroll
       for (int lc = 0; lc < CH / 8; ++lc) {
         uint4 o = make_uint4(0, 0, 0, 0);
-        if (have) {
-          const uint32_t sz = k.z[lc / 4];
-          const uint32_t s2 = __byte_perm(sz, 0u, 0x1010u), z2 = __byte_perm(sz, 0u, 0x3232u);
-          const uint32_t add[4] = {hadd2(z2, mu[lc].x), hadd2(z2, mu[lc].y), hadd2(z2, mu[lc].z), hadd2(z2, mu[lc].w)};
-          o = dequant8(k.w[lc >> 1], lc, s2, add);
+        if (vh) {
+          const uint32_t s2 = __byte_perm(vz[lc / 4], 0u, 0x1010u), z2 = __byte_perm(vz[lc / 4], 0u, 0x3232u);
+          const uint32_t add[4] = {z2, z2, z2, z2};
+          o = dequant8(vw[lc >> 1], lc, s2, add);
         }
-        *reinterpret_cast<uint4*>(kt + sw128_off(row, part * (CH / 8) + lc)) = o;
+        *reinterpret_cast<uint4*>(vt + sw128_off(row, part * (CH / 8) + lc)) = o;
       }
-      store_psac(k, int8, have, row, part, smem + Cfg::OFF_A + st * Cfg::A_BYTES);
       fence_proxy_async();
-      mbar_arrive(bar + B_KFULL + 8 * st);
-      if (first_t) {
-        load_queries(src, b, h, rb, ql);
-        ++seg;
+      mbar_arrive(bar + B_VFULL + 8 * st);
+    };
+    for (; w.more(); w.next(p), ++seg) {
+      const RowsSource& s = p.src[w.src];
+      const int cnt = w.count(), szb = (D >> s.gshift) * 4, r = s.r, top = s.M - 1;
+      const bool int8 = s.psac_fmt == 1, wide = s.M > 256;
+      const uint4* cent4 = reinterpret_cast<const uint4*>(s.cent) + size_t(w.h) * s.M * (D / 8) + part * (CH / 8);
+      const int z_off = row * szb + ((part * CH) >> s.gshift) * 4, z_two = CH >= 64 && s.gshift == 5 ? 4 : 0;
+#pragma unroll 1
+      for (int jj = 0; jj < cnt; ++jj, ++t) {
+        const bool have = (w.j + jj) * kKeys + row < w.len;
+        const int rs = t % Cfg::RS;
+        const uint8_t* raw = smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES;
+        mbar_wait_or_abort(bar + B_RFULL + 8 * rs, (t / Cfg::RS) & 1, p.budget, abort);
+        uint32_t kw[CH / 16], kz[CH >= 64 ? 2 : 1], vw_n[CH / 16], vz_n[CH >= 64 ? 2 : 1], ps[8 / TPR];
+        load_words(raw + row * (D / 4) + part * (CH / 4), kw);
+        load_words(raw + Cfg::RAW_VC + row * (D / 4) + part * (CH / 4), vw_n);
+        kz[0] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_KZ + z_off);
+        vz_n[0] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_VZ + z_off);
+        if constexpr (CH >= 64) {
+          kz[1] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_KZ + z_off + z_two);
+          vz_n[1] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_VZ + z_off + z_two);
+        }
+        const int idx = wide ? reinterpret_cast<const uint16_t*>(raw + Cfg::RAW_IX)[row] : raw[Cfg::RAW_IX + row];
+#pragma unroll
+        for (int i = 0; i < 8 / TPR; ++i) ps[i] = 0u;
+        if (have && part * (16 / TPR) < r) {
+          if (int8) {
+            // fp16(code * the token's scale)
+            uint32_t q[4 / TPR];
+            load_words(raw + Cfg::RAW_PS + row * r + part * (16 / TPR), q);
+            const float sc = __half2float(reinterpret_cast<const __half*>(raw + Cfg::RAW_PSC)[row]);
+#pragma unroll
+            for (int i = 0; i < 8 / TPR; ++i) {
+              const uint32_t two = (q[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+              ps[i] = pack_f16(float(int8_t(two & 0xff)) * sc, float(int8_t(two >> 8)) * sc);
+            }
+          } else {
+            load_words(raw + Cfg::RAW_PS + (row * r + part * (16 / TPR)) * 2, ps);
+          }
+        }
+        // the centre's channels
+        uint4 mu[CH / 8];
+        if (have) {
+          const uint4* m4 = cent4 + size_t(min(idx, top)) * (D / 8);
+#pragma unroll
+          for (int c = 0; c < CH / 8; ++c) mu[c] = __ldg(m4 + c);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + B_REMPTY + 8 * rs);       // the packed tile is read
+        if (t > 0) write_values(t - 1);
+#pragma unroll
+        for (int i = 0; i < CH / 16; ++i) vw[i] = vw_n[i];
+#pragma unroll
+        for (int i = 0; i < (CH >= 64 ? 2 : 1); ++i) vz[i] = vz_n[i];
+        vh = have;
+        const int st = t & 1;
+        if (t >= 2) mbar_wait_or_abort(bar + B_KEMPTY + 8 * st, ((t >> 1) - 1) & 1, p.budget, abort);
+        uint8_t* kt = smem + Cfg::OFF_K + st * Cfg::K_BYTES;
+#pragma unroll
+        for (int lc = 0; lc < CH / 8; ++lc) {
+          uint4 o = make_uint4(0, 0, 0, 0);
+          if (have) {
+            const uint32_t s2 = __byte_perm(kz[lc / 4], 0u, 0x1010u), z2 = __byte_perm(kz[lc / 4], 0u, 0x3232u);
+            const uint32_t add[4] = {hadd2(z2, mu[lc].x), hadd2(z2, mu[lc].y), hadd2(z2, mu[lc].z), hadd2(z2, mu[lc].w)};
+            o = dequant8(kw[lc >> 1], lc, s2, add);
+          }
+          *reinterpret_cast<uint4*>(kt + sw128_off(row, part * (CH / 8) + lc)) = o;
+        }
+        uint8_t* at = smem + Cfg::OFF_A + st * Cfg::A_BYTES + nosw_off(row, part * 2 / TPR) + (part * (16 / TPR) % 8) * 2;
+        if constexpr (TPR == 2) *reinterpret_cast<uint4*>(at) = make_uint4(ps[0], ps[1], ps[2], ps[3]);
+        else *reinterpret_cast<uint2*>(at) = make_uint2(ps[0], ps[1]);
+        fence_proxy_async();
+        mbar_arrive(bar + B_KFULL + 8 * st);
+        if (jj == 0) load_queries();
       }
-      ++t;
-      k = kn;
-      v = vn;
-      vh = have;
-      kh = kh_n;
     }
+    if (t > 0) write_values(t - 1);
   } else {
     // ====== softmax of CPT columns (thread = key = TMEM lane) ======
     const int g = warp >> 2, wq = warp & 3, kl = wq * 32 + lane, bid = 2 + g;
@@ -940,7 +932,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         alpha[kl] = lt > 0.0f ? 1.0f / lt : (lt == 0.0f ? 0.0f : lt);
         if (kl < live) {
           // row of (sequence, query, head) in Q and out
-          const int ri = r0 + kl, row = (w.b * s.Nq + ri / G) * p.H_q + h * G + ri % G;
+          const int ri = r0 + kl, i = p.per_head(ri), row = (w.b * s.Nq + i) * p.H_q + h * G + (ri - i * G);
           row_s[kl] = row;
           if (!whole) p.part_ml[(size_t(blockIdx.x) * 2 + slot) * N + g * CPT + kl] = make_float2(m, lt);
           else if (!p.out) p.dir_ml[size_t(w.src) * p.dir_rows + row] = make_float2(m, lt);
@@ -1225,6 +1217,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
   p.nsrc = a.nsrc;
   p.H_kv = a.src[0].c->H_kv;
   p.H_q = a.H_q;
+  const uint32_t G = uint32_t(a.H_q / p.H_kv);
+  p.g_inv = G > 1 ? uint32_t(((1ull << 32) + G - 1) / G) : 0;
   p.Q = a.Q;
   p.out = a.out;
   p.out_dtype = a.out_dtype;
