@@ -65,7 +65,6 @@ namespace {
 constexpr int kKeys = 128;             // keys per tile (rows of S^T)
 constexpr float kBias = 7.0f;          // p = 2^(x) with x = s log2e - m + kBias
 constexpr float kTrail = 14.0f;        // x above this refreshes the row's running maximum
-constexpr int kStages = 2;
 // A unit begins with kLead positions of the work list that hold no tile: its
 // query rows, first maxima and output rows take about as long as that many key
 // tiles, so parts with many short units get fewer tiles.
@@ -114,7 +113,6 @@ struct RowsParams {
 template <int D, int NT>
 struct RCfg {
   static constexpr int N = NT;
-  static constexpr int X = N == 128 ? 2 : 1, NX = N / X;       // MMA groups of NX columns
   // softmax: 128 threads (keys) per group of CPT columns, so that a thread's
   // sums stay in registers
   static constexpr int CPT = N <= 32 ? 16 : 32, SG = N / CPT, SW = 4 * SG;
@@ -123,25 +121,24 @@ struct RCfg {
   static constexpr int TPR = N == 128 ? 2 : 4, PW = kKeys * TPR / 32;
   static constexpr int kMmaWarp = SW + PW, kLoadWarp = kMmaWarp + 1, kThreads = 32 * (SW + PW + 2);
   static constexpr int CH = D / TPR;                 // channels per producer thread
-  static constexpr int PB = X == 1 ? 2 : 1;          // P buffers per MMA group
-  static constexpr int VS = N == 128 ? 1 : 2;        // value stages (128 rows: what shared memory leaves)
-  static constexpr int RS = N <= 32 ? 3 : 1;         // stages of packed tiles
+  // stages of keys, values, P and packed tiles: what shared memory leaves
+  static constexpr int KS = N == 128 ? 1 : 2, VS = 2, PB = N == 128 ? 1 : 2, RS = N <= 32 ? 3 : 1;
   // packed tile: codes of keys and values, scale and zero words, ids, PSAC
   // (fp16, or int8 codes and from RAW_PSC on the tokens' scales)
   static constexpr int RAW_VC = kKeys * D / 4, RAW_KZ = 2 * RAW_VC, RAW_VZ = RAW_KZ + kKeys * D / 8;
   static constexpr int RAW_IX = RAW_VZ + kKeys * D / 8, RAW_PS = RAW_IX + 2 * kKeys, RAW_PSC = RAW_PS + kKeys * 16;
   static constexpr int RAW_BYTES = RAW_PS + kKeys * 32;
-  static constexpr int Q_BYTES = NX * D * 2, U_BYTES = NX * 32, K_BYTES = kKeys * D * 2, A_BYTES = kKeys * 32;
+  static constexpr int Q_BYTES = N * D * 2, U_BYTES = N * 32, K_BYTES = kKeys * D * 2, A_BYTES = kKeys * 32;
   static constexpr int V_BYTES = kKeys * 256;        // 128 channels (zero above D)
-  static constexpr int P_BYTES = NX * 256;
+  static constexpr int P_BYTES = N * 256;
   static constexpr uint32_t OFF_K = 0;
-  static constexpr uint32_t OFF_V = OFF_K + kStages * K_BYTES;
+  static constexpr uint32_t OFF_V = OFF_K + KS * K_BYTES;
   static constexpr uint32_t OFF_Q = OFF_V + VS * V_BYTES;
-  static constexpr uint32_t OFF_P = OFF_Q + X * Q_BYTES;
-  static constexpr uint32_t OFF_A = OFF_P + X * PB * P_BYTES;
-  static constexpr uint32_t OFF_RAW = OFF_A + kStages * A_BYTES;
+  static constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
+  static constexpr uint32_t OFF_A = OFF_P + PB * P_BYTES;
+  static constexpr uint32_t OFF_RAW = OFF_A + KS * A_BYTES;
   static constexpr uint32_t OFF_U = OFF_RAW + RS * RAW_BYTES;
-  static constexpr uint32_t OFF_FRAG = OFF_U + X * U_BYTES;             // P fragments [D/16][2][2][32] uint2
+  static constexpr uint32_t OFF_FRAG = OFF_U + U_BYTES;             // P fragments [D/16][2][2][32] uint2
   static constexpr uint32_t OFF_SCR = OFF_FRAG + D / 16 * 2 * 2 * 32 * 8;   // row scales, ring of 4 units
   static constexpr uint32_t OFF_QE = OFF_SCR + 4 * N * 4;               // row exponents of the unit being loaded
   static constexpr uint32_t OFF_TAB = OFF_QE + N * 4;                   // per column pair {sc, sc, nm, nm}
@@ -153,9 +150,9 @@ struct RCfg {
   static constexpr uint32_t SMEM = OFF_BAR + 288 + 1024;
   static constexpr uint32_t kTmemUsed = 3 * N;
   static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  // Q and Khat K-major; Vhat by channels; P by rows (NX = 64) or by keys
-  static constexpr uint32_t kIdQK = make_idesc(0, 0, 0, NX, kKeys);
-  static constexpr uint32_t kIdPV = make_idesc(0, 0, NX == 64 ? 1 : 0, NX, 128, 1);
+  // Q and Khat K-major; Vhat by channels; P by rows (64 and more) or by keys
+  static constexpr uint32_t kIdQK = make_idesc(0, 0, 0, N, kKeys);
+  static constexpr uint32_t kIdPV = make_idesc(0, 0, N >= 64 ? 1 : 0, N, 128, 1);
   static_assert(SMEM <= 232448, "shared memory of one CTA");
   static_assert(N == 16 || N == 32 || N == 64 || N == 128, "rows per unit");
 };
@@ -205,6 +202,12 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" 
 // e with |x| < 2^e (finite x; -126 at least), and 2^e
 __device__ __forceinline__ int exp_above(float x) { return int((__float_as_uint(x) >> 23) & 0xffu) - 126; }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// one lane of the warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r != 0;
+}
 // a += the two fp16 values of w
 __device__ __forceinline__ void add_f16x2(float& a, float& b, uint32_t w) {
   asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}\n"
@@ -372,7 +375,7 @@ __device__ __forceinline__ void warp_colsum(float (&v)[NX], int lane) {
 template <int D, int NT>
 __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsParams p) {
   using Cfg = RCfg<D, NT>;
-  constexpr int N = Cfg::N, X = Cfg::X, NX = Cfg::NX, SW = Cfg::SW, PW = Cfg::PW, PB = Cfg::PB;
+  constexpr int N = Cfg::N, SW = Cfg::SW, PW = Cfg::PW, KS = Cfg::KS, VS = Cfg::VS, PB = Cfg::PB;
   constexpr int CH = Cfg::CH, TPR = Cfg::TPR, CPT = Cfg::CPT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -386,23 +389,22 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
   const int G = p.H_q / p.H_kv;
 
   if (tid == 32) {
+    // one arrival per warp of the arriving role, or an MMA commit
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar + B_KFULL + 8 * i, PW * 32);
+      mbar_init(bar + B_KFULL + 8 * i, PW);
       mbar_init(bar + B_KEMPTY + 8 * i, 1);
-      mbar_init(bar + B_VFULL + 8 * i, PW * 32);
+      mbar_init(bar + B_VFULL + 8 * i, PW);
       mbar_init(bar + B_VEMPTY + 8 * i, 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar + B_SFULL + 8 * i, 1);          // [MMA group][buffer]
-      mbar_init(bar + B_SFREE + 8 * i, SW * 32 / X);
-      mbar_init(bar + B_PFULL + 8 * i, SW * 32 / X);
+      mbar_init(bar + B_SFULL + 8 * i, 1);
+      mbar_init(bar + B_SFREE + 8 * i, SW);
+      mbar_init(bar + B_PFULL + 8 * i, SW);
       mbar_init(bar + B_PDONE + 8 * i, 1);
     }
     for (int i = 0; i < Cfg::RS; ++i) {
       mbar_init(bar + B_RFULL + 8 * i, 1);
       mbar_init(bar + B_REMPTY + 8 * i, PW);
     }
-    mbar_init(bar + B_QFULL, PW * 32);
+    mbar_init(bar + B_QFULL, PW);
     mbar_init(bar + B_QEMPTY, 1);
     mbar_init(bar + B_FINAL, 1);
     mbar_init(bar + B_NEVER, 1);
@@ -433,72 +435,66 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
   Walk<N> w = walk_s;
 
   if (warp == Cfg::kMmaWarp) {
-    // ================= MMA issue (one thread) =================
+    // ================= MMA issue =================
+    // The warp's control flow is made uniform by votes and shuffles, so that the
+    // descriptors stay in uniform registers: eight MMAs issue in about 400
+    // cycles, against 630 from a lane picked by its index.
     constexpr uint32_t kIdQK = Cfg::kIdQK, kIdPV = Cfg::kIdPV;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dK = make_sdesc(sb + Cfg::OFF_K, 16, 1024, kLayoutSW128);
     const uint64_t dA = make_sdesc(sb + Cfg::OFF_A, 128, 256, kLayoutNone);
     const uint64_t dV = make_sdesc(sb + Cfg::OFF_V, 16384, 1024, kLayoutSW128);
     const uint64_t dQ = make_sdesc(sb + Cfg::OFF_Q, 16, 1024, kLayoutSW128);
     const uint64_t dU = make_sdesc(sb + Cfg::OFF_U, 128, 256, kLayoutNone);
-    const uint64_t dP = make_sdesc(sb + Cfg::OFF_P, NX == 64 ? 16384 : 16, 1024, kLayoutSW128);
-    bool ok = true;
+    const uint64_t dP = make_sdesc(sb + Cfg::OFF_P, N >= 64 ? 16384 : 16, 1024, kLayoutSW128);
+    auto wait = [&](uint32_t b, uint32_t phase) __attribute__((always_inline)) {
+      return __all_sync(0xffffffffu, mbar_wait_or_abort(bar + b, phase, p.budget, abort)) != 0;
+    };
     int t = 0, seg = 0;
     // P . V of tile tt (the first of its unit's part starts the sums afresh)
-    auto issue_pv = [&](int tt, bool first) __attribute__((always_inline)) -> bool {
-      const int s = tt % Cfg::VS;
-      if (!mbar_wait_or_abort(bar + B_VFULL + 8 * s, (tt / Cfg::VS) & 1, p.budget, abort)) return false;
-      for (int x = 0; x < X; ++x) {
-        const int pb = PB == 2 ? (tt & 1) : 0;
-        const uint32_t par = PB == 2 ? (tt >> 1) & 1 : tt & 1;
-        if (!mbar_wait_or_abort(bar + B_PFULL + 16 * x + 8 * pb, par, p.budget, abort)) return false;
-        fence_after_sync();
-        if (lane == 0) {
-          const uint32_t tO = tmem + 2 * N + x * NX;
-          const uint64_t a = dV + uint64_t(s * Cfg::V_BYTES >> 4);
-          const uint64_t b = dP + uint64_t((x * PB + pb) * Cfg::P_BYTES >> 4);
+    auto issue_pv = [&](int tt, bool first) __attribute__((always_inline)) {
+      const int s = tt % VS, pb = tt % PB;
+      if (!wait(B_VFULL + 8 * s, (tt / VS) & 1)) return false;
+      if (!wait(B_PFULL + 8 * pb, (tt / PB) & 1)) return false;
+      fence_after_sync();
+      if (elect_one()) {
+        const uint64_t a = dV + uint64_t(s * Cfg::V_BYTES >> 4), b = dP + uint64_t(pb * Cfg::P_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) {
-            const uint64_t bo = NX == 64 ? uint64_t(kk * 2048 >> 4) : uint64_t(((kk >> 2) * NX * 128 + (kk & 3) * 32) >> 4);
-            mma_f16(tO, a + uint64_t(kk * 2048 >> 4), b + bo, kIdPV, !(first && kk == 0));
-          }
-          mma_commit(bar + B_PDONE + 16 * x + 8 * pb);
-          if (x == X - 1) mma_commit(bar + B_VEMPTY + 8 * s);
+        for (int kk = 0; kk < kKeys / 16; ++kk) {
+          const uint64_t bo = N >= 64 ? uint64_t(kk * 2048 >> 4) : uint64_t(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4);
+          mma_f16(tm + 2 * N, a + uint64_t(kk * 2048 >> 4), b + bo, kIdPV, kk > 0 || !first);
         }
-        __syncwarp();
+        mma_commit(bar + B_PDONE + 8 * pb);
+        mma_commit(bar + B_VEMPTY + 8 * s);
       }
+      __syncwarp();
       return true;
     };
-    bool pend = false, pend_first = false;      // tile t - 1 still waits for its P . V
-    for (; ok && w.more(); ++seg) {
-      const int cnt = w.count();
-      const bool psac = p.src[w.src].r > 0;
+    bool ok = true, pend = false, pend_first = false;      // pend: tile t - 1 still waits for its P . V
+    for (;; ++seg) {
+      const int cnt = __shfl_sync(0xffffffffu, w.more() ? w.count() : 0, 0);
+      if (cnt == 0) break;
+      const bool psac = __shfl_sync(0xffffffffu, p.src[w.src].r, 0) > 0;
       for (int jj = 0; jj < cnt; ++jj, ++t) {
-        const int s = t & 1;
+        const int s = t % KS, sb2 = t & 1;
         ok = false;
-        if (p.force_timeout && t == 0 && !mbar_wait_or_abort(bar + B_NEVER, 0, p.budget, abort)) break;
+        if (p.force_timeout && t == 0 && !wait(B_NEVER, 0)) break;
         // a unit's last P . V goes before the next unit's first tile, so that
         // its rows can be written while the next queries are multiplied
         if (jj == 0 && pend && !issue_pv(t - 1, pend_first)) break;
-        if (jj == 0 && !mbar_wait_or_abort(bar + B_QFULL, seg & 1, p.budget, abort)) break;
-        if (!mbar_wait_or_abort(bar + B_KFULL + 8 * s, (t >> 1) & 1, p.budget, abort)) break;
-        int x = 0;
-        for (; x < X; ++x) {
-          if (t >= 2 && !mbar_wait_or_abort(bar + B_SFREE + 16 * x + 8 * s, ((t >> 1) - 1) & 1, p.budget, abort)) break;
-          fence_after_sync();
-          if (lane == 0) {
-            const uint32_t tS = tmem + (x * 2 + s) * NX;
-            const uint64_t a = dK + uint64_t(s * Cfg::K_BYTES >> 4), b = dQ + uint64_t(x * Cfg::Q_BYTES >> 4);
+        if (jj == 0 && !wait(B_QFULL, seg & 1)) break;
+        if (!wait(B_KFULL + 8 * s, (t / KS) & 1)) break;
+        if (t >= 2 && !wait(B_SFREE + 8 * sb2, ((t >> 1) - 1) & 1)) break;
+        fence_after_sync();
+        if (elect_one()) {
+          const uint32_t tS = tm + sb2 * N;
+          const uint64_t a = dK + uint64_t(s * Cfg::K_BYTES >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_f16(tS, a + uint64_t(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                      b + uint64_t(((kk >> 2) * NX * 128 + (kk & 3) * 32) >> 4), kIdQK, kk > 0);
-            if (psac) mma_f16(tS, dA + uint64_t(s * Cfg::A_BYTES >> 4), dU + uint64_t(x * Cfg::U_BYTES >> 4), kIdQK, 1);
-            mma_commit(bar + B_SFULL + 16 * x + 8 * s);
-          }
-          __syncwarp();
-        }
-        if (x < X) break;
-        if (lane == 0) {
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16(tS, a + uint64_t(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                    dQ + uint64_t(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4), kIdQK, kk > 0);
+          if (psac) mma_f16(tS, dA + uint64_t(s * Cfg::A_BYTES >> 4), dU, kIdQK, 1);
+          mma_commit(bar + B_SFULL + 8 * sb2);
           mma_commit(bar + B_KEMPTY + 8 * s);
           if (jj == cnt - 1) mma_commit(bar + B_QEMPTY);
         }
@@ -508,6 +504,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         pend_first = jj == 0;
         ok = true;
       }
+      if (!ok) break;
       w.next(p);
     }
     if (ok && pend) issue_pv(t - 1, pend_first);
@@ -560,6 +557,12 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     const int part = TPR == 4 ? lane >> 3 : (lane >> 3) & 1;
     uint2* frag = reinterpret_cast<uint2*>(smem + Cfg::OFF_FRAG);
     int t = 0, seg = 0, frag_src = -1, frag_h = -1;
+    // the warp's operand writes are done: one arrival for all lanes
+    auto arrive_warp = [&](uint32_t b) __attribute__((always_inline)) {
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
+    };
 
     // The query rows of a unit, warp g rows 16 g .. 16 g + 15: copied raw, their
     // product with the basis (bf16 query, exact; P as two bf16 numbers, 2^-16),
@@ -567,16 +570,16 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     auto load_queries = [&]() __attribute__((always_inline)) {
       const RowsSource& s = p.src[w.src];
       constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;       // lanes per row, rows per step, steps
-      const int c = lane % LPR, x = pw * 16 / NX, r0 = pw * 16 % NX;
-      auto q_off = [&](int rx, int ck) { return (ck >> 3) * NX * 128 + rx * 128 + (((ck & 7) ^ (rx & 7)) << 4); };
+      const int c = lane % LPR, r0 = pw * 16;
+      auto q_off = [&](int rx, int ck) { return (ck >> 3) * N * 128 + rx * 128 + (((ck & 7) ^ (rx & 7)) << 4); };
       if (pw < N / 16) {
         if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-          const int rx = r0 + k * RPI + lane / LPR, ri = w.rb * N + x * NX + rx, i = p.per_head(ri);
+          const int rx = r0 + k * RPI + lane / LPR, ri = w.rb * N + rx, i = p.per_head(ri);
           const bool in = ri < w.ql * G;
           const size_t gr = in ? (size_t(w.b) * s.Nq + i) * p.H_q + w.h * G + (ri - i * G) : 0;
-          copy16(sb + Cfg::OFF_Q + x * Cfg::Q_BYTES + q_off(rx, c), p.Q + gr * D + c * 8, in);
+          copy16(sb + Cfg::OFF_Q + q_off(rx, c), p.Q + gr * D + c * 8, in);
         }
       }
       if (s.r > 0 && (w.src != frag_src || w.h != frag_h)) {
@@ -600,7 +603,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         frag_h = w.h;
       }
       if (pw < N / 16) {
-        uint8_t* qt = smem + Cfg::OFF_Q + x * Cfg::Q_BYTES;
+        uint8_t* qt = smem + Cfg::OFF_Q;
         float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + pw * 16;
         int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE) + pw * 16;
         copy_wait();
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t a[4];
-            ldsm_x4(a, sb + Cfg::OFF_Q + x * Cfg::Q_BYTES + q_off(r0 + (lane & 15), 2 * ks + (lane >> 4)));
+            ldsm_x4(a, sb + Cfg::OFF_Q + q_off(r0 + (lane & 15), 2 * ks + (lane >> 4)));
 #pragma unroll
             for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         __syncwarp();
         if (lane < 16) scr[lane] = p.scale_log2 * pow2(-qe[lane]);
         if (s.r > 0) {
-          uint8_t* ut = smem + Cfg::OFF_U + x * Cfg::U_BYTES;
+          uint8_t* ut = smem + Cfg::OFF_U;
           const int ra = lane >> 2, q = (lane & 3) * 4;
           const float ma = pow2(qe[ra]), mb = pow2(qe[ra + 8]);
 #pragma unroll
@@ -668,8 +671,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
           }
         }
       }
-      fence_proxy_async();
-      mbar_arrive(bar + B_QFULL);
+      arrive_warp(bar + B_QFULL);
     };
 
     // Tile by tile: the packed fields move to registers, the centre rows of the
@@ -678,8 +680,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     uint32_t vw[CH / 16], vz[CH >= 64 ? 2 : 1];
     bool vh = false;                             // the thread's token of tile t - 1 exists
     auto write_values = [&](int tt) __attribute__((always_inline)) {
-      const int st = tt % Cfg::VS;
-      if (tt >= Cfg::VS) mbar_wait_or_abort(bar + B_VEMPTY + 8 * st, (tt / Cfg::VS - 1) & 1, p.budget, abort);
+      const int st = tt % VS;
+      if (tt >= VS) mbar_wait_or_abort(bar + B_VEMPTY + 8 * st, (tt / VS - 1) & 1, p.budget, abort);
       uint8_t* vt = smem + Cfg::OFF_V + st * Cfg::V_BYTES;
 #pragma unroll
       for (int lc = 0; lc < CH / 8; ++lc) {
@@ -691,8 +693,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         }
         *reinterpret_cast<uint4*>(vt + sw128_off(row, part * (CH / 8) + lc)) = o;
       }
-      fence_proxy_async();
-      mbar_arrive(bar + B_VFULL + 8 * st);
+      arrive_warp(bar + B_VFULL + 8 * st);
     };
     for (; w.more(); w.next(p), ++seg) {
       const RowsSource& s = p.src[w.src];
@@ -748,8 +749,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
 #pragma unroll
         for (int i = 0; i < (CH >= 64 ? 2 : 1); ++i) vz[i] = vz_n[i];
         vh = have;
-        const int st = t & 1;
-        if (t >= 2) mbar_wait_or_abort(bar + B_KEMPTY + 8 * st, ((t >> 1) - 1) & 1, p.budget, abort);
+        const int st = t % KS;
+        if (t >= KS) mbar_wait_or_abort(bar + B_KEMPTY + 8 * st, (t / KS - 1) & 1, p.budget, abort);
         uint8_t* kt = smem + Cfg::OFF_K + st * Cfg::K_BYTES;
 #pragma unroll
         for (int lc = 0; lc < CH / 8; ++lc) {
@@ -764,8 +765,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         uint8_t* at = smem + Cfg::OFF_A + st * Cfg::A_BYTES + nosw_off(row, part * 2 / TPR) + (part * (16 / TPR) % 8) * 2;
         if constexpr (TPR == 2) *reinterpret_cast<uint4*>(at) = make_uint4(ps[0], ps[1], ps[2], ps[3]);
         else *reinterpret_cast<uint2*>(at) = make_uint2(ps[0], ps[1]);
-        fence_proxy_async();
-        mbar_arrive(bar + B_KFULL + 8 * st);
+        arrive_warp(bar + B_KFULL + 8 * st);
         if (jj == 0) load_queries();
       }
     }
@@ -773,7 +773,6 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
   } else {
     // ====== softmax of CPT columns (thread = key = TMEM lane) ======
     const int g = warp >> 2, wq = warp & 3, kl = wq * 32 + lane, bid = 2 + g;
-    const int x = g * CPT / NX, lc0 = g * CPT % NX;          // MMA group, first column within it
     const uint32_t lane_base = uint32_t(wq * 32) << 16;
     const uint32_t tO = tmem + 2 * N + g * CPT + lane_base;
     float4* tab = reinterpret_cast<float4*>(smem + Cfg::OFF_TAB) + g * (CPT / 2);
@@ -783,8 +782,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     int* row_s = reinterpret_cast<int*>(smem + Cfg::OFF_ROW) + g * CPT;
     float* red = reinterpret_cast<float*>(smem + Cfg::OFF_RED) + g * 4 * CPT;
     auto wait_pv = [&](int tt) {                // P . V of tile tt is complete
-      const int pb = PB == 2 ? (tt & 1) : 0;
-      return mbar_wait_or_abort(bar + B_PDONE + 16 * x + 8 * pb, PB == 2 ? (tt >> 1) & 1 : tt & 1, p.budget, abort);
+      return mbar_wait_or_abort(bar + B_PDONE + 8 * (tt % PB), (tt / PB) & 1, p.budget, abort);
     };
     float l[CPT];
 #pragma unroll
@@ -798,12 +796,12 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       const float* scr = reinterpret_cast<const float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + g * CPT;
       for (int jj = 0; jj < cnt && !gone; ++jj, ++t) {
         const int sbuf = t & 1;
-        const uint32_t tS = tmem + (x * 2 + sbuf) * NX + lc0 + lane_base;
-        dead |= !mbar_wait_or_abort(bar + B_SFULL + 16 * x + 8 * sbuf, (t >> 1) & 1, p.budget, abort);
+        const uint32_t tS = tmem + sbuf * N + g * CPT + lane_base;
+        dead |= !mbar_wait_or_abort(bar + B_SFULL + 8 * sbuf, (t >> 1) & 1, p.budget, abort);
         fence_after_sync();
         const int k0 = (j0 + jj) * kKeys;
         const bool valid = k0 + kl < len, full = k0 + kKeys <= len;
-        uint8_t* pt8 = smem + Cfg::OFF_P + (x * PB + (PB == 2 ? sbuf : 0)) * Cfg::P_BYTES;
+        uint8_t* pt8 = smem + Cfg::OFF_P + (t % PB) * Cfg::P_BYTES;
 #pragma unroll
         for (int c0 = 0; c0 < CPT; c0 += 16) {
           if (gone) break;
@@ -881,7 +879,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
           }
           if (c0 + 16 == CPT) {                   // all scores are read: the buffer may be rewritten
             fence_before_sync();
-            mbar_arrive(bar + B_SFREE + 16 * x + 8 * sbuf);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + B_SFREE + 8 * sbuf);
           }
           // the sums of what enters P . V (the unit's first tile starts them)
 #pragma unroll
@@ -890,17 +889,17 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
             add_f16x2(l[c0 + 2 * i], l[c0 + 2 * i + 1], pw[i]);
           }
           if (c0 == 0 && t >= PB) dead |= !wait_pv(t - PB);    // the buffer is free
-          if constexpr (NX == 64) {
-            // rows along the operand's contiguous dimension: [key][64 rows], swizzled
-            const int ck = (lc0 + c0) / 8;
-            *reinterpret_cast<uint4*>(pt8 + kl * 128 + ((ck ^ (kl & 7)) << 4)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-            *reinterpret_cast<uint4*>(pt8 + kl * 128 + (((ck + 1) ^ (kl & 7)) << 4)) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
+          if constexpr (N >= 64) {
+            // rows along the operand's contiguous dimension: [N / 64][key][64 rows], swizzled
+            const int ck = (g * CPT + c0) / 8;
+            *reinterpret_cast<uint4*>(pt8 + sw128_off(kl, ck)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            *reinterpret_cast<uint4*>(pt8 + sw128_off(kl, ck + 1)) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
           } else {
             // keys along the contiguous dimension: [2][row][64 keys], swizzled
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int rr = lc0 + c0 + i;
-              *reinterpret_cast<uint16_t*>(pt8 + (kl >> 6) * NX * 128 + rr * 128 + ((((kl & 63) >> 3) ^ (rr & 7)) << 4) +
+              const int rr = g * CPT + c0 + i;
+              *reinterpret_cast<uint16_t*>(pt8 + (kl >> 6) * N * 128 + rr * 128 + ((((kl & 63) >> 3) ^ (rr & 7)) << 4) +
                                            (kl & 7) * 2) = uint16_t((i & 1) ? pw[i / 2] >> 16 : pw[i / 2] & 0xffffu);
             }
           }
@@ -908,7 +907,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         if (gone) break;
         fence_proxy_async();
         fence_before_sync();
-        mbar_arrive(bar + B_PFULL + 16 * x + 8 * (PB == 2 ? sbuf : 0));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + B_PFULL + 8 * (t % PB));
       }
       // ---- the unit's rows
       if (!gone) {
@@ -978,7 +978,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
   __syncthreads();
   if (warp == Cfg::kMmaWarp) {
     if (*abort) {
-      if (lane == 0) {
+      if (elect_one()) {                          // (the lane that issued the MMAs)
         atomicExch(p.err, 1);
         mma_commit(bar + B_FINAL);                // wait (bounded) for MMAs in flight
       }
