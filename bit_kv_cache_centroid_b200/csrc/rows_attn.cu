@@ -116,10 +116,12 @@ struct RCfg {
   // softmax: 128 threads (keys) per group of CPT columns, so that a thread's
   // sums stay in registers
   static constexpr int CPT = N <= 32 ? 16 : 32, SG = N / CPT, SW = 4 * SG;
-  // producers: 4 threads per key (16 warps hide the loads' latency); at 128
-  // rows, where the softmax has 16 warps, 2
-  static constexpr int TPR = N == 128 ? 2 : 4, PW = kKeys * TPR / 32;
-  static constexpr int kMmaWarp = SW + PW, kLoadWarp = kMmaWarp + 1, kThreads = 32 * (SW + PW + 2);
+  // producers: TPR threads per key for keys, as many for values (apart, so that
+  // the waits and loads of one overlap the arithmetic of the other); with 16
+  // softmax warps one
+  static constexpr int TPR = N == 128 ? 1 : 2, PW = 4 * TPR;
+  static constexpr int kValueWarp = SW + PW, kMmaWarp = SW + 2 * PW, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (SW + 2 * PW + 2);
   static constexpr int CH = D / TPR;                 // channels per producer thread
   // stages of keys, values, P and packed tiles: what shared memory leaves
   static constexpr int KS = N == 128 ? 1 : 2, VS = 2, PB = N == 128 ? 1 : 2, RS = N <= 32 ? 3 : 1;
@@ -326,17 +328,18 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
 // producers
 // ---------------------------------------------------------------------------
 
-// N consecutive 32-bit words of shared memory
+// W consecutive 32-bit words of shared memory
 template <int W>
-__device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[W]) {
-  if constexpr (W == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-  } else if constexpr (W == 2) {
+__device__ __forceinline__ void load_words(const uint8_t* src, uint32_t* w) {
+  if constexpr (W == 2) {
     const uint2 v = *reinterpret_cast<const uint2*>(src);
     w[0] = v.x; w[1] = v.y;
   } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(src);
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + 4 * i);
+      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+    }
   }
 }
 
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     }
     for (int i = 0; i < Cfg::RS; ++i) {
       mbar_init(bar + B_RFULL + 8 * i, 1);
-      mbar_init(bar + B_REMPTY + 8 * i, PW);
+      mbar_init(bar + B_REMPTY + 8 * i, 2 * PW);
     }
     mbar_init(bar + B_QFULL, PW);
     mbar_init(bar + B_QEMPTY, 1);
@@ -550,11 +553,13 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     }
   } else if (warp >= SW) {
     // ================= producers =================
-    // lanes 8q..8q+7 of a warp take 8 consecutive keys and one part of their
-    // channels: their 16-byte stores fall on 8 distinct swizzled bank groups
-    const int pt = tid - SW * 32, pw = pt >> 5;
-    const int row = TPR == 4 ? pw * 8 + (lane & 7) : pw * 16 + (lane & 7) + 8 * (lane >> 4);
-    const int part = TPR == 4 ? lane >> 3 : (lane >> 3) & 1;
+    // With two threads per key, lanes 8q..8q+7 of a warp take 8 consecutive keys
+    // and one half of their channels; with one, 32 keys. Either way the 16-byte
+    // stores of 8 lanes fall on 8 distinct swizzled bank groups.
+    const bool values = warp >= Cfg::kValueWarp;
+    const int pt = tid - (values ? Cfg::kValueWarp : SW) * 32, pw = pt >> 5;
+    const int row = TPR == 2 ? pw * 16 + (lane & 7) + 8 * (lane >> 4) : pt;
+    const int part = TPR == 2 ? (lane >> 3) & 1 : 0;
     uint2* frag = reinterpret_cast<uint2*>(smem + Cfg::OFF_FRAG);
     int t = 0, seg = 0, frag_src = -1, frag_h = -1;
     // the warp's operand writes are done: one arrival for all lanes
@@ -564,16 +569,16 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       if (lane == 0) mbar_arrive(b);
     };
 
-    // The query rows of a unit, warp g rows 16 g .. 16 g + 15: copied raw, their
+    // The query rows of a unit (by the value warps, 16 rows a warp): copied raw, their
     // product with the basis (bf16 query, exact; P as two bf16 numbers, 2^-16),
     // then both scaled by 2^e per row, max(|q|, |u|) 2^e < 2^15, to fp16.
     auto load_queries = [&]() __attribute__((always_inline)) {
       const RowsSource& s = p.src[w.src];
       constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;       // lanes per row, rows per step, steps
-      const int c = lane % LPR, r0 = pw * 16;
+      const int c = lane % LPR;
       auto q_off = [&](int rx, int ck) { return (ck >> 3) * N * 128 + rx * 128 + (((ck & 7) ^ (rx & 7)) << 4); };
-      if (pw < N / 16) {
-        if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
+      if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
+      for (int r0 = pw * 16; r0 < N; r0 += PW * 16) {
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
           const int rx = r0 + k * RPI + lane / LPR, ri = w.rb * N + rx, i = p.per_head(ri);
@@ -602,12 +607,12 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         frag_src = w.src;
         frag_h = w.h;
       }
-      if (pw < N / 16) {
+      copy_wait();
+      __syncwarp();
+      for (int r0 = pw * 16; r0 < N; r0 += PW * 16) {
         uint8_t* qt = smem + Cfg::OFF_Q;
-        float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + pw * 16;
-        int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE) + pw * 16;
-        copy_wait();
-        __syncwarp();
+        float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + r0;
+        int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE) + r0;
         float acc[2][4] = {};
         if (s.r > 0) {
 #pragma unroll
@@ -674,102 +679,126 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       arrive_warp(bar + B_QFULL);
     };
 
-    // Tile by tile: the packed fields move to registers, the centre rows of the
-    // tile's ids are requested, the values of tile t - 1 are written meanwhile,
-    // then the keys of tile t.
-    uint32_t vw[CH / 16], vz[CH >= 64 ? 2 : 1];
-    bool vh = false;                             // the thread's token of tile t - 1 exists
-    auto write_values = [&](int tt) __attribute__((always_inline)) {
-      const int st = tt % VS;
-      if (tt >= VS) mbar_wait_or_abort(bar + B_VEMPTY + 8 * st, (tt / VS - 1) & 1, p.budget, abort);
-      uint8_t* vt = smem + Cfg::OFF_V + st * Cfg::V_BYTES;
-#pragma unroll
-      for (int lc = 0; lc < CH / 8; ++lc) {
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (vh) {
-          const uint32_t s2 = __byte_perm(vz[lc / 4], 0u, 0x1010u), z2 = __byte_perm(vz[lc / 4], 0u, 0x3232u);
-          const uint32_t add[4] = {z2, z2, z2, z2};
-          o = dequant8(vw[lc >> 1], lc, s2, add);
-        }
-        *reinterpret_cast<uint4*>(vt + sw128_off(row, part * (CH / 8) + lc)) = o;
-      }
-      arrive_warp(bar + B_VFULL + 8 * st);
+    constexpr int W = CH / 16, Q32 = CH / 32;     // code words, 32-channel runs of a thread
+    // byte offset of the scale/zero word of the thread's run q
+    auto z_off = [&](int szb, int gshift, int q) __attribute__((always_inline)) {
+      return row * szb + ((part * CH + 32 * q) >> gshift) * 4;
     };
     for (; w.more(); w.next(p), ++seg) {
       const RowsSource& s = p.src[w.src];
-      const int cnt = w.count(), szb = (D >> s.gshift) * 4, r = s.r, top = s.M - 1;
-      const bool int8 = s.psac_fmt == 1, wide = s.M > 256;
-      const uint4* cent4 = reinterpret_cast<const uint4*>(s.cent) + size_t(w.h) * s.M * (D / 8) + part * (CH / 8);
-      const int z_off = row * szb + ((part * CH) >> s.gshift) * 4, z_two = CH >= 64 && s.gshift == 5 ? 4 : 0;
+      const int cnt = w.count(), gshift = s.gshift, szb = (D >> gshift) * 4;
+      if (values) {
+        load_queries();
 #pragma unroll 1
-      for (int jj = 0; jj < cnt; ++jj, ++t) {
-        const bool have = (w.j + jj) * kKeys + row < w.len;
-        const int rs = t % Cfg::RS;
-        const uint8_t* raw = smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES;
-        mbar_wait_or_abort(bar + B_RFULL + 8 * rs, (t / Cfg::RS) & 1, p.budget, abort);
-        uint32_t kw[CH / 16], kz[CH >= 64 ? 2 : 1], vw_n[CH / 16], vz_n[CH >= 64 ? 2 : 1], ps[8 / TPR];
-        load_words(raw + row * (D / 4) + part * (CH / 4), kw);
-        load_words(raw + Cfg::RAW_VC + row * (D / 4) + part * (CH / 4), vw_n);
-        kz[0] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_KZ + z_off);
-        vz_n[0] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_VZ + z_off);
-        if constexpr (CH >= 64) {
-          kz[1] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_KZ + z_off + z_two);
-          vz_n[1] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_VZ + z_off + z_two);
-        }
-        const int idx = wide ? reinterpret_cast<const uint16_t*>(raw + Cfg::RAW_IX)[row] : raw[Cfg::RAW_IX + row];
+        for (int jj = 0; jj < cnt; ++jj, ++t) {
+          const bool have = (w.j + jj) * kKeys + row < w.len;
+          const int rs = t % Cfg::RS, st = t % VS;
+          const uint8_t* raw = smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES;
+          mbar_wait_or_abort(bar + B_RFULL + 8 * rs, (t / Cfg::RS) & 1, p.budget, abort);
+          uint32_t vw[W], vz[Q32];
+          load_words<W>(raw + Cfg::RAW_VC + row * (D / 4) + part * (CH / 4), vw);
 #pragma unroll
-        for (int i = 0; i < 8 / TPR; ++i) ps[i] = 0u;
-        if (have && part * (16 / TPR) < r) {
-          if (int8) {
-            // fp16(code * the token's scale)
-            uint32_t q[4 / TPR];
-            load_words(raw + Cfg::RAW_PS + row * r + part * (16 / TPR), q);
-            const float sc = __half2float(reinterpret_cast<const __half*>(raw + Cfg::RAW_PSC)[row]);
+          for (int q = 0; q < Q32; ++q) vz[q] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_VZ + z_off(szb, gshift, q));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar + B_REMPTY + 8 * rs);       // the packed tile's values are read
+          if (!have) {                            // a code of zero, scale and zero of zero
 #pragma unroll
-            for (int i = 0; i < 8 / TPR; ++i) {
-              const uint32_t two = (q[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-              ps[i] = pack_f16(float(int8_t(two & 0xff)) * sc, float(int8_t(two >> 8)) * sc);
-            }
-          } else {
-            load_words(raw + Cfg::RAW_PS + (row * r + part * (16 / TPR)) * 2, ps);
+            for (int q = 0; q < Q32; ++q) vz[q] = 0u;
           }
+          if (t >= VS) mbar_wait_or_abort(bar + B_VEMPTY + 8 * st, (t / VS - 1) & 1, p.budget, abort);
+          uint8_t* vt = smem + Cfg::OFF_V + st * Cfg::V_BYTES;
+#pragma unroll
+          for (int q = 0; q < Q32; ++q) {
+            const uint32_t s2 = __byte_perm(vz[q], 0u, 0x1010u), z2 = __byte_perm(vz[q], 0u, 0x3232u);
+            const uint32_t add[4] = {z2, z2, z2, z2};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(vt + sw128_off(row, part * (CH / 8) + 4 * q + c)) =
+                  dequant8(vw[2 * q + (c >> 1)], c, s2, add);
+          }
+          arrive_warp(bar + B_VFULL + 8 * st);
         }
-        // the centre's channels
-        uint4 mu[CH / 8];
-        if (have) {
-          const uint4* m4 = cent4 + size_t(min(idx, top)) * (D / 8);
+      } else {
+        const uint4* cent4 = reinterpret_cast<const uint4*>(s.cent) + size_t(w.h) * s.M * (D / 8) + part * (CH / 8);
+        const int r = s.r, top = s.M - 1;
+        const bool int8 = s.psac_fmt == 1, wide = s.M > 256;
+        constexpr int CP = 16 / TPR;              // PSAC coefficients of a thread
+#pragma unroll 1
+        for (int jj = 0; jj < cnt; ++jj, ++t) {
+          const bool have = (w.j + jj) * kKeys + row < w.len;
+          const int rs = t % Cfg::RS, st = t % KS;
+          const uint8_t* raw = smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES;
+          mbar_wait_or_abort(bar + B_RFULL + 8 * rs, (t / Cfg::RS) & 1, p.budget, abort);
+          const int id = wide ? reinterpret_cast<const uint16_t*>(raw + Cfg::RAW_IX)[row] : raw[Cfg::RAW_IX + row];
+          // (an id is only followed where the token exists)
+          const uint4* m4 = cent4 + size_t(have ? min(id, top) : 0) * (D / 8);
+          uint4 mu[4];
 #pragma unroll
-          for (int c = 0; c < CH / 8; ++c) mu[c] = __ldg(m4 + c);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar + B_REMPTY + 8 * rs);       // the packed tile is read
-        if (t > 0) write_values(t - 1);
+          for (int c = 0; c < 4; ++c) mu[c] = __ldg(m4 + c);
+          uint32_t kw[W], kz[Q32], ps[CP / 2];
+          load_words<W>(raw + row * (D / 4) + part * (CH / 4), kw);
 #pragma unroll
-        for (int i = 0; i < CH / 16; ++i) vw[i] = vw_n[i];
+          for (int q = 0; q < Q32; ++q) kz[q] = *reinterpret_cast<const uint32_t*>(raw + Cfg::RAW_KZ + z_off(szb, gshift, q));
 #pragma unroll
-        for (int i = 0; i < (CH >= 64 ? 2 : 1); ++i) vz[i] = vz_n[i];
-        vh = have;
-        const int st = t % KS;
-        if (t >= KS) mbar_wait_or_abort(bar + B_KEMPTY + 8 * st, (t / KS - 1) & 1, p.budget, abort);
-        uint8_t* kt = smem + Cfg::OFF_K + st * Cfg::K_BYTES;
-#pragma unroll
-        for (int lc = 0; lc < CH / 8; ++lc) {
-          uint4 o = make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < CP / 2; ++i) ps[i] = 0u;
           if (have) {
-            const uint32_t s2 = __byte_perm(kz[lc / 4], 0u, 0x1010u), z2 = __byte_perm(kz[lc / 4], 0u, 0x3232u);
-            const uint32_t add[4] = {hadd2(z2, mu[lc].x), hadd2(z2, mu[lc].y), hadd2(z2, mu[lc].z), hadd2(z2, mu[lc].w)};
-            o = dequant8(kw[lc >> 1], lc, s2, add);
+            if (int8) {
+              // fp16(code * the token's scale)
+              const float sc = __half2float(reinterpret_cast<const __half*>(raw + Cfg::RAW_PSC)[row]);
+#pragma unroll
+              for (int e = 0; e < CP; e += 8) {
+                if (part * CP + e < r) {
+                  const uint2 two = *reinterpret_cast<const uint2*>(raw + Cfg::RAW_PS + row * r + part * CP + e);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint32_t q = ((i < 2 ? two.x : two.y) >> (16 * (i & 1))) & 0xffffu;
+                    ps[e / 2 + i] = pack_f16(float(int8_t(q & 0xff)) * sc, float(int8_t(q >> 8)) * sc);
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < CP; e += 8)
+                if (part * CP + e < r) load_words<4>(raw + Cfg::RAW_PS + (row * r + part * CP + e) * 2, ps + e / 2);
+            }
           }
-          *reinterpret_cast<uint4*>(kt + sw128_off(row, part * (CH / 8) + lc)) = o;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar + B_REMPTY + 8 * rs);       // the packed tile's keys are read
+          if (!have) {                            // codes, scale, zero and centre of zero
+#pragma unroll
+            for (int q = 0; q < Q32; ++q) kz[q] = 0u;
+          }
+          if (t >= KS) mbar_wait_or_abort(bar + B_KEMPTY + 8 * st, (t / KS - 1) & 1, p.budget, abort);
+          uint8_t* kt = smem + Cfg::OFF_K + st * Cfg::K_BYTES;
+#pragma unroll
+          for (int q = 0; q < Q32; ++q) {
+            uint4 next[4];
+            if (q + 1 < Q32) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) next[c] = __ldg(m4 + 4 * (q + 1) + c);
+            }
+            const uint32_t s2 = __byte_perm(kz[q], 0u, 0x1010u), z2 = __byte_perm(kz[q], 0u, 0x3232u);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint4 m = have ? mu[c] : make_uint4(0, 0, 0, 0);
+              const uint32_t add[4] = {hadd2(z2, m.x), hadd2(z2, m.y), hadd2(z2, m.z), hadd2(z2, m.w)};
+              *reinterpret_cast<uint4*>(kt + sw128_off(row, part * (CH / 8) + 4 * q + c)) =
+                  dequant8(kw[2 * q + (c >> 1)], c, s2, add);
+            }
+            if (q + 1 < Q32) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) mu[c] = next[c];
+            }
+          }
+          uint8_t* at = smem + Cfg::OFF_A + st * Cfg::A_BYTES;
+#pragma unroll
+          for (int e = 0; e < CP; e += 8)
+            *reinterpret_cast<uint4*>(at + nosw_off(row, (part * CP + e) / 8)) =
+                make_uint4(ps[e / 2], ps[e / 2 + 1], ps[e / 2 + 2], ps[e / 2 + 3]);
+          arrive_warp(bar + B_KFULL + 8 * st);
         }
-        uint8_t* at = smem + Cfg::OFF_A + st * Cfg::A_BYTES + nosw_off(row, part * 2 / TPR) + (part * (16 / TPR) % 8) * 2;
-        if constexpr (TPR == 2) *reinterpret_cast<uint4*>(at) = make_uint4(ps[0], ps[1], ps[2], ps[3]);
-        else *reinterpret_cast<uint2*>(at) = make_uint2(ps[0], ps[1]);
-        arrive_warp(bar + B_KFULL + 8 * st);
-        if (jj == 0) load_queries();
       }
     }
-    if (t > 0) write_values(t - 1);
   } else {
     // ====== softmax of CPT columns (thread = key = TMEM lane) ======
     const int g = warp >> 2, wq = warp & 3, kl = wq * 32 + lane, bid = 2 + g;

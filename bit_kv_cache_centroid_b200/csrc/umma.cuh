@@ -60,6 +60,7 @@ __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.
 // flag; a wait that runs out raises it.
 __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t phase, unsigned long long budget,
                                                    volatile int* abort) {
+  if (mbar_try(bar, phase)) return true;
   const unsigned long long t0 = clock64();
   while (!mbar_try(bar, phase)) {
     if (*abort) return false;
