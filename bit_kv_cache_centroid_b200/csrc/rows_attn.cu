@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
   constexpr int N = Cfg::N, SW = Cfg::SW, PW = Cfg::PW, KS = Cfg::KS, VS = Cfg::VS, PB = Cfg::PB;
   constexpr int CH = Cfg::CH, TPR = Cfg::TPR, CPT = Cfg::CPT;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (by pointer arithmetic, so that accesses stay shared-memory accesses)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
   const uint32_t bar = sb + Cfg::OFF_BAR;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAR + B_TMEM);
