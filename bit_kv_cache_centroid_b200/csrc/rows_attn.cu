@@ -121,7 +121,16 @@ struct RCfg {
   // softmax warps one
   static constexpr int TPR = N == 128 ? 1 : 2, PW = 4 * TPR;
   static constexpr int kValueWarp = SW + PW, kMmaWarp = SW + 2 * PW, kLoadWarp = kMmaWarp + 1;
-  static constexpr int kThreads = 32 * (SW + 2 * PW + 2);
+  // (whole warpgroups, so that they can trade registers)
+  static constexpr int kThreads = 32 * (SW + 2 * PW + 4);
+  // registers per thread by role, in all the launch's threads times kRegs: the
+  // softmax keeps its sums, one per column, and must not spill them
+  static constexpr int kRegs = N == 16 ? 80 : 72;
+  static constexpr int kRegsSoft = N == 16 || N == 64 ? 96 : 80;
+  static constexpr int kRegsProd = N == 16 ? 80 : N == 32 ? 72 : 64;
+  static constexpr int kRegsIssue = 56;
+  static_assert(SW * kRegsSoft + 2 * PW * kRegsProd + 4 * kRegsIssue <= (SW + 2 * PW + 4) * kRegs,
+                "register split");
   static constexpr int CH = D / TPR;                 // channels per producer thread
   // stages of keys, values, P and packed tiles: what shared memory leaves
   static constexpr int KS = N == 128 ? 1 : 2, VS = 2, PB = N == 128 ? 1 : 2, RS = N <= 32 ? 3 : 1;
@@ -204,6 +213,12 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" 
 // e with |x| < 2^e (finite x; -126 at least), and 2^e
 __device__ __forceinline__ int exp_above(float x) { return int((__float_as_uint(x) >> 23) & 0xffu) - 126; }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// this warpgroup's registers per thread: R, of the launch's LAUNCHED
+template <int R, int LAUNCHED>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (R > LAUNCHED) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  if constexpr (R < LAUNCHED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
 // one lane of the warp
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -438,7 +453,9 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
   const uint32_t tmem = *tmem_slot;
   Walk<N> w = walk_s;
 
-  if (warp == Cfg::kMmaWarp) {
+  if (warp >= Cfg::kMmaWarp) {
+    set_regs<Cfg::kRegsIssue, Cfg::kRegs>();
+    if (warp == Cfg::kMmaWarp) {
     // ================= MMA issue =================
     // The warp's control flow is made uniform by votes and shuffles, so that the
     // descriptors stay in uniform registers: eight MMAs issue in about 400
@@ -512,7 +529,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       w.next(p);
     }
     if (ok && pend) issue_pv(t - 1, pend_first);
-  } else if (warp == Cfg::kLoadWarp) {
+    } else if (warp == Cfg::kLoadWarp) {
     // ================= packed tiles (one thread, bulk copies) =================
     if (lane == 0) {
       int t = 0;
@@ -552,8 +569,10 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       for (int i = max(0, t - Cfg::RS); i < t; ++i)
         mbar_wait(bar + B_RFULL + 8 * (i % Cfg::RS), (i / Cfg::RS) & 1, p.budget);
     }
+    }
   } else if (warp >= SW) {
     // ================= producers =================
+    set_regs<Cfg::kRegsProd, Cfg::kRegs>();
     // With two threads per key, lanes 8q..8q+7 of a warp take 8 consecutive keys
     // and one half of their channels; with one, 32 keys. Either way the 16-byte
     // stores of 8 lanes fall on 8 distinct swizzled bank groups.
@@ -802,6 +821,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     }
   } else {
     // ====== softmax of CPT columns (thread = key = TMEM lane) ======
+    set_regs<Cfg::kRegsSoft, Cfg::kRegs>();
     const int g = warp >> 2, wq = warp & 3, kl = wq * 32 + lane, bid = 2 + g;
     const uint32_t lane_base = uint32_t(wq * 32) << 16;
     const uint32_t tO = tmem + 2 * N + g * CPT + lane_base;
@@ -1194,6 +1214,11 @@ cudaError_t launch_cfg(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) 
   auto kern = rows_attn_kernel<D, N>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg::SMEM));
   if (e != cudaSuccess) return e;
+  // the role split spends exactly these registers: with fewer at launch it would wait for ever
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != Cfg::kRegs) return cudaErrorInvalidConfiguration;
   RowsParams q = p;
   if (p.nsrc == 2) q.out = nullptr;
   kern<<<pl.C, Cfg::kThreads, Cfg::SMEM, s>>>(q);
