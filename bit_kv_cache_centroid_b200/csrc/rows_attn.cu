@@ -150,7 +150,8 @@ struct RCfg {
   static constexpr uint32_t OFF_RAW = OFF_A + KS * A_BYTES;
   static constexpr uint32_t OFF_U = OFF_RAW + RS * RAW_BYTES;
   static constexpr uint32_t OFF_FRAG = OFF_U + U_BYTES;             // P fragments [D/16][2][2][32] uint2
-  static constexpr uint32_t OFF_SCR = OFF_FRAG + D / 16 * 2 * 2 * 32 * 8;   // row scales, ring of 4 units
+  static constexpr uint32_t OFF_UF = OFF_FRAG + D / 16 * 2 * 2 * 32 * 8;    // fp32 products of more row blocks than warps
+  static constexpr uint32_t OFF_SCR = OFF_UF + (N > PW * 16 ? N * 64 : 0);  // row scales, ring of 4 units
   static constexpr uint32_t OFF_QE = OFF_SCR + 4 * N * 4;               // row exponents of the unit being loaded
   static constexpr uint32_t OFF_TAB = OFF_QE + N * 4;                   // per column pair {sc, sc, nm, nm}
   static constexpr uint32_t OFF_MROW = OFF_TAB + N * 8;
@@ -237,8 +238,11 @@ __device__ __forceinline__ void add_f16x2(float& a, float& b, uint32_t w) {
 // ---------------------------------------------------------------------------
 
 // first position of CTA c of C over T positions, and the CTA that holds position u
-__device__ __forceinline__ long long part_begin(long long T, int c, int C) { return T * c / C; }
-__device__ __forceinline__ int part_of(long long u, long long T, int C) { return int(((u + 1) * C - 1) / T); }
+__device__ __forceinline__ long long quot(long long a, long long b) {       // of non-negative numbers
+  return ((a | b) >> 32) == 0 ? static_cast<long long>(uint32_t(a) / uint32_t(b)) : a / b;
+}
+__device__ __forceinline__ long long part_begin(long long T, int c, int C) { return quot(T * c, C); }
+__device__ __forceinline__ int part_of(long long u, long long T, int C) { return int(quot((u + 1) * C - 1, T)); }
 
 // keys and queries of a sequence
 __device__ __forceinline__ int seq_len(const RowsSource& s, int b) {
@@ -317,7 +321,7 @@ __device__ void plan(const RowsParams& p, int lane, Walk<N>& w) {
             w.b = b0 + l;
             const long long rem = lo - (at + __shfl_sync(0xffffffffu, inc - v, l));
             w.load(p);
-            const int unit = tiles_of(w.len) + kLead, in = int(rem % unit), ub = int(rem / unit);
+            const int unit = tiles_of(w.len) + kLead, ub = int(quot(rem, unit)), in = int(rem - static_cast<long long>(ub) * unit);
             const int RB = blocks_of<N>(w.ql, G);
             w.h = ub / RB;
             w.rb = ub % RB;
@@ -589,56 +593,59 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       if (lane == 0) mbar_arrive(b);
     };
 
-    // The query rows of a unit (by the value warps, 16 rows a warp): copied raw, their
-    // product with the basis (bf16 query, exact; P as two bf16 numbers, 2^-16),
-    // then both scaled by 2^e per row, max(|q|, |u|) 2^e < 2^15, to fp16.
+    // The query rows of a unit, by the value warps: copied raw, 16 bytes per
+    // thread and step; their product with the basis (bf16 query, exact; P as two
+    // bf16 numbers, 2^-16), 16 rows per warp; then both scaled by 2^e per row,
+    // max(|q|, |u|) 2^e < 2^15, to fp16.
     auto load_queries = [&]() __attribute__((always_inline)) {
       const RowsSource& s = p.src[w.src];
-      constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;       // lanes per row, rows per step, steps
-      const int c = lane % LPR;
-      auto q_off = [&](int rx, int ck) { return (ck >> 3) * N * 128 + rx * 128 + (((ck & 7) ^ (rx & 7)) << 4); };
+      constexpr int LPR = D / 8, STEP = PW * 32 / LPR;      // lanes per row, rows per step
+      const int c = pt % LPR, r0 = pt / LPR;
+      uint8_t* qt = smem + Cfg::OFF_Q;
+      float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N;
+      int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE);
+      auto q_off = [&](int rx, int k) { return (k >> 3) * N * 128 + rx * 128 + (((k & 7) ^ (rx & 7)) << 4); };
       if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
-      for (int r0 = pw * 16; r0 < N; r0 += PW * 16) {
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-          const int rx = r0 + k * RPI + lane / LPR, ri = w.rb * N + rx, i = p.per_head(ri);
-          const bool in = ri < w.ql * G;
-          const size_t gr = in ? (size_t(w.b) * s.Nq + i) * p.H_q + w.h * G + (ri - i * G) : 0;
-          copy16(sb + Cfg::OFF_Q + q_off(rx, c), p.Q + gr * D + c * 8, in);
-        }
+#pragma unroll 1
+      for (int rx = r0; rx < N; rx += STEP) {
+        const int ri = w.rb * N + rx, i = p.per_head(ri);
+        const bool in = ri < w.ql * G;
+        const size_t gr = in ? (size_t(w.b) * s.Nq + i) * p.H_q + w.h * G + (ri - i * G) : 0;
+        copy16(sb + Cfg::OFF_Q + q_off(rx, c), p.Q + gr * D + c * 8, in);
       }
-      if (s.r > 0 && (w.src != frag_src || w.h != frag_h)) {
-        const float* Ph = s.P + size_t(w.h) * D * s.r;
-        bar_sync(1, PW * 32);                     // the previous fragments are read
-        for (int i = pt; i < D / 16 * 2 * 32; i += PW * 32) {
-          const int l = i & 31, nt = (i >> 5) & 1, ks = i >> 6;
-          const int n = nt * 8 + (l >> 2), c = ks * 16 + 2 * (l & 3);
-          float hi[4], lo[4];
+      float acc[2][4];
+      if (s.r > 0) {
+        if (w.src != frag_src || w.h != frag_h) {
+          const float* Ph = s.P + size_t(w.h) * D * s.r;
+#pragma unroll 1
+          for (int i = pt; i < D / 16 * 2 * 32; i += PW * 32) {
+            const int l = i & 31, nt = (i >> 5) & 1, ks = i >> 6;
+            const int n = nt * 8 + (l >> 2), k = ks * 16 + 2 * (l & 3);
+            float hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = n < s.r ? __ldg(Ph + size_t(c + (e & 1) + 8 * (e >> 1)) * s.r + n) : 0.0f;
-            hi[e] = __bfloat162float(__float2bfloat16_rn(y));
-            lo[e] = y - hi[e];
+            for (int e = 0; e < 4; ++e) {
+              const float y = n < s.r ? __ldg(Ph + size_t(k + (e & 1) + 8 * (e >> 1)) * s.r + n) : 0.0f;
+              hi[e] = __bfloat162float(__float2bfloat16_rn(y));
+              lo[e] = y - hi[e];
+            }
+            frag[((ks * 2 + nt) * 2 + 0) * 32 + l] = make_uint2(pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3]));
+            frag[((ks * 2 + nt) * 2 + 1) * 32 + l] = make_uint2(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]));
           }
-          frag[((ks * 2 + nt) * 2 + 0) * 32 + l] = make_uint2(pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3]));
-          frag[((ks * 2 + nt) * 2 + 1) * 32 + l] = make_uint2(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]));
+          frag_src = w.src;
+          frag_h = w.h;
         }
-        bar_sync(1, PW * 32);
-        frag_src = w.src;
-        frag_h = w.h;
-      }
-      copy_wait();
-      __syncwarp();
-      for (int r0 = pw * 16; r0 < N; r0 += PW * 16) {
-        uint8_t* qt = smem + Cfg::OFF_Q;
-        float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + r0;
-        int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE) + r0;
-        float acc[2][4] = {};
-        if (s.r > 0) {
+        copy_wait();
+        bar_sync(1, PW * 32);                     // rows and fragments are there
+#pragma unroll 1
+        for (int rb = pw * 16; rb < N; rb += PW * 16) {
 #pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[nt][k] = 0.0f;
+#pragma unroll 2
           for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t a[4];
-            ldsm_x4(a, sb + Cfg::OFF_Q + q_off(r0 + (lane & 15), 2 * ks + (lane >> 4)));
+            ldsm_x4(a, sb + Cfg::OFF_Q + q_off(rb + (lane & 15), 2 * ks + (lane >> 4)));
 #pragma unroll
             for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
@@ -647,52 +654,79 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
                 mma16816(acc[nt], a, bb.x, bb.y);
               }
           }
+          // largest |u| of rows lane / 4 and lane / 4 + 8, for the threads that scale them
+          float u0 = fmaxf(fmaxf(fabsf(acc[0][0]), fabsf(acc[0][1])), fmaxf(fabsf(acc[1][0]), fabsf(acc[1][1])));
+          float u1 = fmaxf(fmaxf(fabsf(acc[0][2]), fabsf(acc[0][3])), fmaxf(fabsf(acc[1][2]), fabsf(acc[1][3])));
+#pragma unroll
+          for (int o = 1; o <= 2; o <<= 1) {
+            u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
+            u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
+          }
+          if ((lane & 3) == 0) {
+            scr[rb + (lane >> 2)] = u0;
+            scr[rb + (lane >> 2) + 8] = u1;
+          }
+          if constexpr (N > PW * 16) {
+            // more blocks than warps: kept in shared memory until they are scaled
+            float* uf = reinterpret_cast<float*>(smem + Cfg::OFF_UF) + rb * 16;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const int n = nt * 8 + 2 * (lane & 3);
+              *reinterpret_cast<float2*>(uf + (lane >> 2) * 16 + n) = make_float2(acc[nt][0], acc[nt][1]);
+              *reinterpret_cast<float2*>(uf + ((lane >> 2) + 8) * 16 + n) = make_float2(acc[nt][2], acc[nt][3]);
+            }
+          }
         }
-        // largest |u| of rows lane / 4 and lane / 4 + 8, for the lanes that scale them
-        float u0 = fmaxf(fmaxf(fabsf(acc[0][0]), fabsf(acc[0][1])), fmaxf(fabsf(acc[1][0]), fabsf(acc[1][1])));
-        float u1 = fmaxf(fmaxf(fabsf(acc[0][2]), fabsf(acc[0][3])), fmaxf(fabsf(acc[1][2]), fabsf(acc[1][3])));
+        bar_sync(1, PW * 32);                     // the raw rows are read
+      } else {
+        copy_wait();
+      }
+#pragma unroll 1
+      for (int rx = r0; rx < N; rx += STEP) {
+        uint4* at = reinterpret_cast<uint4*>(qt + q_off(rx, c));
+        const uint4 v = *at;
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        uint32_t am = 0;
 #pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-          u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
-          u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
+        for (int i = 0; i < 4; ++i) am = __vmaxu2(am, u[i] & 0x7fff7fffu);
+        am = max(am & 0xffffu, am >> 16);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+        const float top = fmaxf(__uint_as_float(am << 16), s.r > 0 ? scr[rx] : 0.0f);
+        const int e = top > 0.0f && top < INFINITY && am < 0x7f80u ? min(max(15 - exp_above(top), -126), 64) : 0;
+        const float qmul = pow2(e);
+        uint32_t o4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o4[i] = pack_f16(__uint_as_float(u[i] << 16) * qmul, __uint_as_float(u[i] & 0xffff0000u) * qmul);
+        *at = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+        __syncwarp();                             // scr[rx] is read by the row's lanes
+        if (c == 0) {
+          qe[rx] = e;
+          scr[rx] = p.scale_log2 * pow2(-e);
         }
-        if ((lane & 3) == 0) {
-          scr[lane >> 2] = u0;
-          scr[(lane >> 2) + 8] = u1;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-          const int rr = k * RPI + lane / LPR;
-          uint4* at = reinterpret_cast<uint4*>(qt + q_off(r0 + rr, c));
-          const uint4 v = *at;
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-          uint32_t am = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) am = __vmaxu2(am, u[i] & 0x7fff7fffu);
-          am = max(am & 0xffffu, am >> 16);
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-          const float top = fmaxf(__uint_as_float(am << 16), scr[rr]);
-          const int e = top > 0.0f && top < INFINITY && am < 0x7f80u ? min(max(15 - exp_above(top), -126), 64) : 0;
-          const float qmul = pow2(e);
-          uint32_t o4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o4[i] = pack_f16(__uint_as_float(u[i] << 16) * qmul, __uint_as_float(u[i] & 0xffff0000u) * qmul);
-          *at = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-          if (c == 0) qe[rr] = e;
-        }
-        __syncwarp();
-        if (lane < 16) scr[lane] = p.scale_log2 * pow2(-qe[lane]);
-        if (s.r > 0) {
+      }
+      if (s.r > 0) {
+        bar_sync(1, PW * 32);                     // the rows' exponents are there
+#pragma unroll 1
+        for (int rb = pw * 16; rb < N; rb += PW * 16) {
           uint8_t* ut = smem + Cfg::OFF_U;
-          const int ra = lane >> 2, q = (lane & 3) * 4;
+          const int ra = rb + (lane >> 2), q = (lane & 3) * 4;
+          if constexpr (N > PW * 16) {
+            const float* uf = reinterpret_cast<const float*>(smem + Cfg::OFF_UF) + rb * 16;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const int n = nt * 8 + 2 * (lane & 3);
+              const float2 x = *reinterpret_cast<const float2*>(uf + (lane >> 2) * 16 + n);
+              const float2 y = *reinterpret_cast<const float2*>(uf + ((lane >> 2) + 8) * 16 + n);
+              acc[nt][0] = x.x; acc[nt][1] = x.y; acc[nt][2] = y.x; acc[nt][3] = y.y;
+            }
+          }
           const float ma = pow2(qe[ra]), mb = pow2(qe[ra + 8]);
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
-            *reinterpret_cast<uint32_t*>(ut + nosw_off(r0 + ra, nt) + q) = pack_f16(acc[nt][0] * ma, acc[nt][1] * ma);
-            *reinterpret_cast<uint32_t*>(ut + nosw_off(r0 + ra + 8, nt) + q) = pack_f16(acc[nt][2] * mb, acc[nt][3] * mb);
+            *reinterpret_cast<uint32_t*>(ut + nosw_off(ra, nt) + q) = pack_f16(acc[nt][0] * ma, acc[nt][1] * ma);
+            *reinterpret_cast<uint32_t*>(ut + nosw_off(ra + 8, nt) + q) = pack_f16(acc[nt][2] * mb, acc[nt][3] * mb);
           }
         }
       }
