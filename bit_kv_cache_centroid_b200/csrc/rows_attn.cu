@@ -12,35 +12,36 @@
 //
 //   s_rt = (q_r . khat_t + u_r . a_t) sm_scale,   o_r = sum_t softmax_t(s_r) vhat_t.
 //
-// Both products are computed transposed, keys (then channels) in the 128 rows
-// of the tensor-core tile and the queries in its N columns,
+// with tcgen05: S [128 rows x 128 keys] = Q . Khat^T + U . A^T into TMEM, the
+// softmax by a thread per row, P back into the columns of S, O += P . Vhat in
+// TMEM. Operands are fp16 as in the chunk kernel: Khat = fp16(code s +
+// fp16(z + mu)), Vhat = fp16(code s + z) with exact codes, one rounding per fp16
+// operation; queries scaled per row by a power of two, which leaves bf16 values
+// exact; U = fp16 of an fp32 product of the bf16 query with P in two bf16
+// halves; P = fp16(p).
 //
-//   S^T [128 keys x N]     = Khat [128 x d] . Q^T  + A [128 x 16] . U^T
-//   O^T [128 channels x N] += Vhat^T [d x 128 keys] . P^T,
+// Two softmax groups of four warps keep the tensor core and the exponentials
+// busy in turn. With more than 128 rows (WIDE, units of 256 rows) each group has
+// 128 rows of its own, and every dequantized tile serves both. With fewer, both
+// groups have the same 128 rows and take the tiles alternately, each with its
+// own S, O, maximum and sum, joined when the unit's rows are written; rows that
+// do not exist cost their warps nothing. (A transposed form, keys in the tile's
+// rows and the queries in as few columns as there are, was built and measured
+// first: its per-column maxima and sums cost about 13,000 warp instructions per
+// 128 x 128 scores, against 4,000 here, and the tensor core's time, which it
+// saves for few rows, is not what bounds either.)
 //
-// so that a few rows cost a few columns (N = 16..64 per group of softmax
-// warps) and the softmax's work spreads over 128 threads, one per key,
-// whatever the number of rows. A key behind the sequence's end is then one
-// thread whose probabilities are zero.
+// Softmax: p = 2^(s log2e - m_r + 7) against a running maximum m_r that may
+// trail the true one by 2^7: p stays below 2^14 and keeps 21 binary orders of
+// normal fp16 below the maximum, and O is rescaled only when a row's scores pass
+// m_r by more than that. m_r is a whole number: every rescaling is by an exact
+// power of two, and p's rounding does not depend on where the work is cut.
 //
-// Softmax without a maximum per tile: p = 2^(s log2e - m_r + 7) is taken
-// against a running maximum m_r that may trail the true one by 2^7, so p stays
-// below 2^14 and keeps 21 binary orders of normal fp16 below the maximum. Only
-// when a score passes m_r by more than 7 (always on a unit's first tile) the
-// group takes the tile's maxima per column and rescales its sums and O. Sums
-// are fp32: l in registers of the key's thread, O in TMEM.
-//
-// Operands are fp16 as in the chunk kernel: Khat = fp16(code s + fp16(z + mu)),
-// Vhat = fp16(code s + z) with exact codes, one rounding per fp16 operation;
-// queries scaled per row by a power of two, which leaves bf16 values exact;
-// U = fp16 of the fp32 product of the scaled fp16 query with P in two fp16
-// halves; P^T = fp16(p).
-//
-// Warp roles of a CTA (one per SM): 4 softmax warps per row group; 8 or 16
-// producer warps (packed fields -> swizzled fp16 operand tiles, two stages;
-// query tiles at the start of a unit); one warp that issues the MMAs. S^T is
-// double-buffered in TMEM, so the keys of tile t + 1 are multiplied while tile
-// t is in the softmax.
+// Warp roles of a CTA (one per SM): 8 softmax warps; 8 warps that dequantize
+// keys and 8 for values (the latter also load the unit's queries), so that the
+// waits and loads of one overlap the arithmetic of the other; one warp that
+// issues the MMAs, polling both groups; one thread that copies packed tiles to
+// shared memory. Registers are traded between the roles' warpgroups.
 //
 // Work: the key tiles of all units form one list (source, sequence, KV head,
 // row block, tile), of which every CTA takes an equal contiguous part, found
@@ -52,6 +53,7 @@
 // ends the other waits, the workspace's first word is set, the rows of the
 // CTA's remaining part become NaN and the kernel ends.
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "internal.h"
@@ -62,9 +64,10 @@
 namespace kv2 {
 namespace {
 
-constexpr int kKeys = 128;             // keys per tile (rows of S^T)
+constexpr int kKeys = 128;             // keys per tile
+constexpr int kRows = 128;             // rows per softmax group (TMEM lanes)
 constexpr float kBias = 7.0f;          // p = 2^(x) with x = s log2e - m + kBias
-constexpr float kTrail = 14.0f;        // x above this refreshes the row's running maximum
+constexpr float kTrail = 7.0f;         // a score this far above the running maximum moves it
 // A unit begins with kLead positions of the work list that hold no tile: its
 // query rows, first maxima and output rows take about as long as that many key
 // tiles, so parts with many short units get fewer tiles.
@@ -95,7 +98,7 @@ struct RowsParams {
   const uint16_t* Q;        // bf16 [rows of (b, i)][H_q][D]
   void* out;                // null: whole units go to dir_o / dir_ml
   int out_dtype;
-  float scale_log2;
+  float scale_log2, q_sign; // |sm_scale| log2(e), and sm_scale's sign, which the queries take
   int* err;
   long long* total;         // workspace: length of the work list
   long long* base;          // workspace: first position of every sequence, [src 0 | src 1]
@@ -109,76 +112,51 @@ struct RowsParams {
   int force_timeout;
 };
 
-// D channels, N rows per unit (columns of S^T)
-template <int D, int NT>
+// D channels; WIDE: units of 256 rows, else of 128
+template <int D, bool WIDE>
 struct RCfg {
-  static constexpr int N = NT;
-  // softmax: 128 threads (keys) per group of CPT columns, so that a thread's
-  // sums stay in registers
-  static constexpr int CPT = N <= 32 ? 16 : 32, SG = N / CPT, SW = 4 * SG;
-  // producers: TPR threads per key for keys, as many for values (apart, so that
-  // the waits and loads of one overlap the arithmetic of the other); with 16
-  // softmax warps one
-  static constexpr int TPR = N == 128 ? 1 : 2, PW = 4 * TPR;
+  static constexpr int X = WIDE ? 2 : 1, N = kRows * X;
+  static constexpr int SW = 8, PW = 8, CH = D / 2;           // warps per role; channels per producer thread
   static constexpr int kValueWarp = SW + PW, kMmaWarp = SW + 2 * PW, kLoadWarp = kMmaWarp + 1;
   // (whole warpgroups, so that they can trade registers)
   static constexpr int kThreads = 32 * (SW + 2 * PW + 4);
-  // registers per thread by role, in all the launch's threads times kRegs: the
-  // softmax keeps its sums, one per column, and must not spill them
-  static constexpr int kRegs = N == 16 ? 80 : 72;
-  static constexpr int kRegsSoft = N == 16 || N == 64 ? 96 : 80;
-  static constexpr int kRegsProd = N == 16 ? 80 : N == 32 ? 72 : 64;
-  static constexpr int kRegsIssue = 56;
-  static_assert(SW * kRegsSoft + 2 * PW * kRegsProd + 4 * kRegsIssue <= (SW + 2 * PW + 4) * kRegs,
-                "register split");
-  static constexpr int CH = D / TPR;                 // channels per producer thread
-  // stages of keys, values, P and packed tiles: what shared memory leaves
-  static constexpr int KS = N == 128 ? 1 : 2, VS = 2, PB = N == 128 ? 1 : 2, RS = N <= 32 ? 3 : 1;
+  // registers per thread by role, in all the launch's threads times kRegs
+  static constexpr int kRegs = 72, kRegsSoft = 88, kRegsProd = 64, kRegsIssue = 72;
+  static_assert(SW * kRegsSoft + 2 * PW * kRegsProd + 4 * kRegsIssue <= (SW + 2 * PW + 4) * kRegs, "register split");
+  // stages of keys, values and packed tiles. With WIDE units the keys of tile
+  // t + 1 are multiplied after P . V of tile t, a softmax later than they could
+  // first be written: one stage is enough.
+  static constexpr int KS = WIDE ? 1 : 2, VS = WIDE ? 1 : 2, RS = WIDE ? 3 : 2;
   // packed tile: codes of keys and values, scale and zero words, ids, PSAC
   // (fp16, or int8 codes and from RAW_PSC on the tokens' scales)
   static constexpr int RAW_VC = kKeys * D / 4, RAW_KZ = 2 * RAW_VC, RAW_VZ = RAW_KZ + kKeys * D / 8;
   static constexpr int RAW_IX = RAW_VZ + kKeys * D / 8, RAW_PS = RAW_IX + 2 * kKeys, RAW_PSC = RAW_PS + kKeys * 16;
   static constexpr int RAW_BYTES = RAW_PS + kKeys * 32;
-  static constexpr int Q_BYTES = N * D * 2, U_BYTES = N * 32, K_BYTES = kKeys * D * 2, A_BYTES = kKeys * 32;
-  static constexpr int V_BYTES = kKeys * 256;        // 128 channels (zero above D)
-  static constexpr int P_BYTES = N * 256;
+  static constexpr int Q_BYTES = kRows * D * 2, U_BYTES = kRows * 32, K_BYTES = kKeys * D * 2, A_BYTES = kKeys * 32;
+  static constexpr int V_BYTES = kKeys * D * 2;
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_V = OFF_K + KS * K_BYTES;
   static constexpr uint32_t OFF_Q = OFF_V + VS * V_BYTES;
-  static constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
-  static constexpr uint32_t OFF_A = OFF_P + PB * P_BYTES;
+  static constexpr uint32_t OFF_A = OFF_Q + X * Q_BYTES;
   static constexpr uint32_t OFF_RAW = OFF_A + KS * A_BYTES;
   static constexpr uint32_t OFF_U = OFF_RAW + RS * RAW_BYTES;
-  static constexpr uint32_t OFF_FRAG = OFF_U + U_BYTES;             // P fragments [D/16][2][2][32] uint2
+  static constexpr uint32_t OFF_FRAG = OFF_U + X * U_BYTES;             // P fragments [D/16][2][2][32] uint2
   static constexpr uint32_t OFF_UF = OFF_FRAG + D / 16 * 2 * 2 * 32 * 8;    // fp32 products of more row blocks than warps
   static constexpr uint32_t OFF_SCR = OFF_UF + (N > PW * 16 ? N * 64 : 0);  // row scales, ring of 4 units
   static constexpr uint32_t OFF_QE = OFF_SCR + 4 * N * 4;               // row exponents of the unit being loaded
-  static constexpr uint32_t OFF_TAB = OFF_QE + N * 4;                   // per column pair {sc, sc, nm, nm}
-  static constexpr uint32_t OFF_MROW = OFF_TAB + N * 8;
-  static constexpr uint32_t OFF_ALPHA = OFF_MROW + N * 4;
-  static constexpr uint32_t OFF_ROW = OFF_ALPHA + N * 4;                // row of Q and out per column
-  static constexpr uint32_t OFF_RED = OFF_ROW + N * 4;                  // [SG][4 warps][CPT]
-  static constexpr uint32_t OFF_BAR = OFF_RED + 4 * N * 4;
+  static constexpr uint32_t OFF_ML = OFF_QE + N * 4;                    // maxima and sums of both groups, float2 [2][kRows]
+  static constexpr uint32_t OFF_BAR = OFF_ML + 2 * kRows * 8;
   static constexpr uint32_t SMEM = OFF_BAR + 288 + 1024;
-  static constexpr uint32_t kTmemUsed = 3 * N;
-  static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  // Q and Khat K-major; Vhat by channels; P by rows (64 and more) or by keys
-  static constexpr uint32_t kIdQK = make_idesc(0, 0, 0, N, kKeys);
-  static constexpr uint32_t kIdPV = make_idesc(0, 0, N >= 64 ? 1 : 0, N, 128, 1);
+  static constexpr uint32_t kTmemCols = 512;           // S of both groups, O of both groups
+  // Q, U, Khat, A K-major; Vhat by channels
+  static constexpr uint32_t kIdQK = make_idesc(0, 0, 0, kKeys, kRows);
+  static constexpr uint32_t kIdPV = make_idesc(0, 0, 1, D, kRows);
   static_assert(SMEM <= 232448, "shared memory of one CTA");
-  static_assert(N == 16 || N == 32 || N == 64 || N == 128, "rows per unit");
 };
 // barrier slots (bytes from OFF_BAR)
-constexpr uint32_t B_KFULL = 0, B_KEMPTY = 16, B_VFULL = 32, B_VEMPTY = 48, B_SFULL = 64, B_SFREE = 96,
-                   B_PFULL = 128, B_PDONE = 160, B_QFULL = 192, B_QEMPTY = 200, B_FINAL = 208, B_NEVER = 216,
+constexpr uint32_t B_KFULL = 0, B_KEMPTY = 16, B_VFULL = 32, B_VEMPTY = 48, B_SFULL = 64, B_PFULL = 96,
+                   B_PDONE = 128, B_QFULL = 192, B_QEMPTY = 200, B_FINAL = 208, B_NEVER = 216,
                    B_TMEM = 224, B_ABORT = 228, B_RFULL = 232, B_REMPTY = 256;
-
-// order-preserving map of floats to signed integers, and back
-__device__ __forceinline__ int f2ord(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float ord2f(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
 __device__ __forceinline__ void bar_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
@@ -206,6 +184,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// whether the barrier's phase of this parity has completed (no wait)
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t phase) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred P1;\n\tmbarrier.test_wait.parity.shared::cta.b64 P1, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, P1;\n\t}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(phase)
+      : "memory");
+  return done != 0;
+}
 // 16 bytes global -> shared by the asynchronous copy (zeros when !ok)
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
@@ -226,13 +215,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
   return r != 0;
 }
-// a += the two fp16 values of w
-__device__ __forceinline__ void add_f16x2(float& a, float& b, uint32_t w) {
-  asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}\n"
-      : "+f"(a), "+f"(b)
-      : "r"(w));
-}
-
 // ---------------------------------------------------------------------------
 // the work list: every unit is kLead positions, then one per key tile
 // ---------------------------------------------------------------------------
@@ -372,33 +354,10 @@ __device__ __forceinline__ uint4 dequant8(uint32_t word, int lc, uint32_t s2, co
 }
 
 // ---------------------------------------------------------------------------
-// column sums over the warp's lanes (keys): afterwards lane c holds column c's
-// sum in v[0] (16 columns: lanes c and c + 16)
-// ---------------------------------------------------------------------------
-template <int NX>
-__device__ __forceinline__ void warp_colsum(float (&v)[NX], int lane) {
-  static_assert(NX == 16 || NX == 32, "columns");
-  if constexpr (NX == 16) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
-  }
-#pragma unroll
-  for (int o = NX / 2; o > 0; o >>= 1) {
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float a = v[i], b = v[i + o];
-      const bool up = (lane & o) != 0;
-      v[i] = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, o);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-template <int D, int NT>
-__global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsParams p) {
-  using Cfg = RCfg<D, NT>;
-  constexpr int N = Cfg::N, SW = Cfg::SW, PW = Cfg::PW, KS = Cfg::KS, VS = Cfg::VS, PB = Cfg::PB;
-  constexpr int CH = Cfg::CH, TPR = Cfg::TPR, CPT = Cfg::CPT;
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsParams p) {
+  using Cfg = RCfg<D, WIDE>;
+  constexpr int N = Cfg::N, SW = Cfg::SW, PW = Cfg::PW, KS = Cfg::KS, VS = Cfg::VS, CH = Cfg::CH;
   extern __shared__ uint8_t smem_raw[];
   // (by pointer arithmetic, so that accesses stay shared-memory accesses)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -418,9 +377,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       mbar_init(bar + B_KEMPTY + 8 * i, 1);
       mbar_init(bar + B_VFULL + 8 * i, PW);
       mbar_init(bar + B_VEMPTY + 8 * i, 1);
-      mbar_init(bar + B_SFULL + 8 * i, 1);
-      mbar_init(bar + B_SFREE + 8 * i, SW);
-      mbar_init(bar + B_PFULL + 8 * i, SW);
+      mbar_init(bar + B_SFULL + 8 * i, 1);        // per softmax group
+      mbar_init(bar + B_PFULL + 8 * i, SW / 2);
       mbar_init(bar + B_PDONE + 8 * i, 1);
     }
     for (int i = 0; i < Cfg::RS; ++i) {
@@ -444,13 +402,6 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       p.cta[blockIdx.x] = make_int4(w.src, w.b, w.h * blocks_of<N>(w.ql, G) + w.rb, w.j);
     }
   }
-  if constexpr (D < 128) {
-    // the channels above D of the value stages stay zero
-    for (int i = tid; i < Cfg::VS * kKeys * 8; i += Cfg::kThreads)
-      *reinterpret_cast<uint4*>(smem + Cfg::OFF_V + (i / (kKeys * 8)) * Cfg::V_BYTES + 16384 + (i % (kKeys * 8)) * 16) =
-          make_uint4(0, 0, 0, 0);
-    fence_proxy_async();
-  }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -463,7 +414,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     // ================= MMA issue =================
     // The warp's control flow is made uniform by votes and shuffles, so that the
     // descriptors stay in uniform registers: eight MMAs issue in about 400
-    // cycles, against 630 from a lane picked by its index.
+    // cycles, against 630 from a lane picked by its index. Both groups are
+    // polled, so that neither waits for the other's softmax.
     constexpr uint32_t kIdQK = Cfg::kIdQK, kIdPV = Cfg::kIdPV;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dK = make_sdesc(sb + Cfg::OFF_K, 16, 1024, kLayoutSW128);
@@ -471,68 +423,105 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
     const uint64_t dV = make_sdesc(sb + Cfg::OFF_V, 16384, 1024, kLayoutSW128);
     const uint64_t dQ = make_sdesc(sb + Cfg::OFF_Q, 16, 1024, kLayoutSW128);
     const uint64_t dU = make_sdesc(sb + Cfg::OFF_U, 128, 256, kLayoutNone);
-    const uint64_t dP = make_sdesc(sb + Cfg::OFF_P, N >= 64 ? 16384 : 16, 1024, kLayoutSW128);
-    auto wait = [&](uint32_t b, uint32_t phase) __attribute__((always_inline)) {
-      return __all_sync(0xffffffffu, mbar_wait_or_abort(bar + b, phase, p.budget, abort)) != 0;
+    auto ready = [&](uint32_t b, uint32_t phase) __attribute__((always_inline)) {
+      return __all_sync(0xffffffffu, mbar_test(bar + b, phase)) != 0;
     };
-    int t = 0, seg = 0;
-    // P . V of tile tt (the first of its unit's part starts the sums afresh)
-    auto issue_pv = [&](int tt, bool first) __attribute__((always_inline)) {
-      const int s = tt % VS, pb = tt % PB;
-      if (!wait(B_VFULL + 8 * s, (tt / VS) & 1)) return false;
-      if (!wait(B_PFULL + 8 * pb, (tt / PB) & 1)) return false;
-      fence_after_sync();
-      if (elect_one()) {
-        const uint64_t a = dV + uint64_t(s * Cfg::V_BYTES >> 4), b = dP + uint64_t(pb * Cfg::P_BYTES >> 4);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk) {
-          const uint64_t bo = N >= 64 ? uint64_t(kk * 2048 >> 4) : uint64_t(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4);
-          mma_f16(tm + 2 * N, a + uint64_t(kk * 2048 >> 4), b + bo, kIdPV, kk > 0 || !first);
-        }
-        mma_commit(bar + B_PDONE + 8 * pb);
-        mma_commit(bar + B_VEMPTY + 8 * s);
+    // a group's next tile: t counts the CTA's tiles, jj the part's tiles of the unit
+    struct Cursor {
+      Walk<N> w;
+      int cnt, jj, t, seg;
+      bool psac, pv;                             // pv: the tile's scores are issued, P . V is next
+    } cur[2];
+    auto settle = [&](Cursor& c) __attribute__((always_inline)) {   // to the unit that holds the tile
+      for (;;) {
+        c.cnt = __shfl_sync(0xffffffffu, c.w.more() ? c.w.count() : 0, 0);
+        if (c.cnt == 0) return;
+        if (c.jj < c.cnt) break;
+        c.jj -= c.cnt;
+        ++c.seg;
+        c.w.next(p);
       }
-      __syncwarp();
-      return true;
+      c.psac = __shfl_sync(0xffffffffu, p.src[c.w.src].r, 0) > 0;
     };
-    bool ok = true, pend = false, pend_first = false;      // pend: tile t - 1 still waits for its P . V
-    for (;; ++seg) {
-      const int cnt = __shfl_sync(0xffffffffu, w.more() ? w.count() : 0, 0);
-      if (cnt == 0) break;
-      const bool psac = __shfl_sync(0xffffffffu, p.src[w.src].r, 0) > 0;
-      for (int jj = 0; jj < cnt; ++jj, ++t) {
-        const int s = t % KS, sb2 = t & 1;
-        ok = false;
-        if (p.force_timeout && t == 0 && !wait(B_NEVER, 0)) break;
-        // a unit's last P . V goes before the next unit's first tile, so that
-        // its rows can be written while the next queries are multiplied
-        if (jj == 0 && pend && !issue_pv(t - 1, pend_first)) break;
-        if (jj == 0 && !wait(B_QFULL, seg & 1)) break;
-        if (!wait(B_KFULL + 8 * s, (t / KS) & 1)) break;
-        if (t >= 2 && !wait(B_SFREE + 8 * sb2, ((t >> 1) - 1) & 1)) break;
-        fence_after_sync();
-        if (elect_one()) {
-          const uint32_t tS = tm + sb2 * N;
-          const uint64_t a = dK + uint64_t(s * Cfg::K_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16(tS, a + uint64_t(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                    dQ + uint64_t(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4), kIdQK, kk > 0);
-          if (psac) mma_f16(tS, dA + uint64_t(s * Cfg::A_BYTES >> 4), dU, kIdQK, 1);
-          mma_commit(bar + B_SFULL + 8 * sb2);
-          mma_commit(bar + B_KEMPTY + 8 * s);
-          if (jj == cnt - 1) mma_commit(bar + B_QEMPTY);
-        }
-        __syncwarp();
-        if (jj > 0 && !issue_pv(t - 1, pend_first)) break;
-        pend = true;
-        pend_first = jj == 0;
-        ok = true;
-      }
-      if (!ok) break;
-      w.next(p);
+    for (int x = 0; x < 2; ++x) {
+      cur[x].w = w;
+      cur[x].t = cur[x].jj = WIDE ? 0 : x;
+      cur[x].seg = 0;
+      cur[x].pv = cur[x].psac = false;
+      settle(cur[x]);
     }
-    if (ok && pend) issue_pv(t - 1, pend_first);
+    int scores = 0;                               // tiles whose scores are issued (by the only group that takes them)
+    unsigned long long since = clock64();
+    bool ok = true;
+    if (p.force_timeout) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar + B_NEVER, 0, p.budget, abort));
+    while (ok && (cur[0].cnt || cur[1].cnt)) {
+      bool moved = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        Cursor& c = cur[x];
+        Cursor& o = cur[1 - x];
+        if (c.cnt == 0) continue;
+        const int k = WIDE ? c.t : c.t >> 1;      // the group's tiles before this one
+        const uint32_t tS = tm + x * kKeys, tO = tm + 2 * kKeys + x * kRows;
+        // with WIDE units, whether the other group is past this tile's step
+        const bool other_s = !WIDE || o.cnt == 0 || o.t > c.t || (o.t == c.t && o.pv);
+        const bool other_v = !WIDE || o.cnt == 0 || o.t > c.t;
+        if (!c.pv) {
+          const int s = c.t % KS;
+          if (!WIDE && scores != c.t) continue;   // in the order of the tiles
+          if (k > 0 && !ready(B_PDONE + 8 * x, (k - 1) & 1)) continue;     // P lies in the columns of S
+          if (!ready(B_KFULL + 8 * s, (c.t / KS) & 1)) continue;
+          if (!ready(B_QFULL, c.seg & 1)) continue;
+          fence_after_sync();
+          if (elect_one()) {
+            const uint64_t a = dQ + uint64_t((WIDE ? x * Cfg::Q_BYTES : 0) >> 4), b = dK + uint64_t(s * Cfg::K_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = uint64_t(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+              mma_f16(tS, a + off, b + off, kIdQK, kk > 0);
+            }
+            if (c.psac)
+              mma_f16(tS, dU + uint64_t((WIDE ? x * Cfg::U_BYTES : 0) >> 4), dA + uint64_t(s * Cfg::A_BYTES >> 4), kIdQK, 1);
+            mma_commit(bar + B_SFULL + 8 * x);
+            if (other_s) {
+              mma_commit(bar + B_KEMPTY + 8 * s);
+              if (c.jj == c.cnt - 1) mma_commit(bar + B_QEMPTY);
+            }
+          }
+          __syncwarp();
+          ++scores;
+          c.pv = true;
+          moved = true;
+        } else {
+          const int s = c.t % VS;
+          if (!ready(B_PFULL + 8 * x, k & 1)) continue;
+          if (!ready(B_VFULL + 8 * s, (c.t / VS) & 1)) continue;
+          fence_after_sync();
+          if (elect_one()) {
+            const bool first = c.jj < (WIDE ? 1 : 2);    // the group's first tile of the unit's part
+            const uint64_t b = dV + uint64_t(s * Cfg::V_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_f16_tmem_a(tO, tS + kk * 8, b + uint64_t(kk * 2048 >> 4), kIdPV, kk > 0 || !first);
+            mma_commit(bar + B_PDONE + 8 * x);
+            if (other_v) mma_commit(bar + B_VEMPTY + 8 * s);
+          }
+          __syncwarp();
+          c.pv = false;
+          c.t += WIDE ? 1 : 2;
+          c.jj += WIDE ? 1 : 2;
+          settle(c);
+          moved = true;
+        }
+      }
+      const unsigned long long now = clock64();
+      if (moved) since = now;
+      else if (__any_sync(0xffffffffu, *abort || now - since > p.budget)) {
+        *abort = 1;
+        ok = false;
+      }
+    }
     } else if (warp == Cfg::kLoadWarp) {
     // ================= packed tiles (one thread, bulk copies) =================
     if (lane == 0) {
@@ -577,13 +566,12 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
   } else if (warp >= SW) {
     // ================= producers =================
     set_regs<Cfg::kRegsProd, Cfg::kRegs>();
-    // With two threads per key, lanes 8q..8q+7 of a warp take 8 consecutive keys
-    // and one half of their channels; with one, 32 keys. Either way the 16-byte
-    // stores of 8 lanes fall on 8 distinct swizzled bank groups.
+    // Two threads per key: lanes 8q..8q+7 of a warp take 8 consecutive keys and
+    // one half of their channels, so that the 16-byte stores of 8 lanes fall on 8
+    // distinct swizzled bank groups.
     const bool values = warp >= Cfg::kValueWarp;
     const int pt = tid - (values ? Cfg::kValueWarp : SW) * 32, pw = pt >> 5;
-    const int row = TPR == 2 ? pw * 16 + (lane & 7) + 8 * (lane >> 4) : pt;
-    const int part = TPR == 2 ? (lane >> 3) & 1 : 0;
+    const int row = pw * 16 + (lane & 7) + 8 * (lane >> 4), part = (lane >> 3) & 1;
     uint2* frag = reinterpret_cast<uint2*>(smem + Cfg::OFF_FRAG);
     int t = 0, seg = 0, frag_src = -1, frag_h = -1;
     // the warp's operand writes are done: one arrival for all lanes
@@ -604,10 +592,12 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       uint8_t* qt = smem + Cfg::OFF_Q;
       float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N;
       int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE);
-      auto q_off = [&](int rx, int k) { return (k >> 3) * N * 128 + rx * 128 + (((k & 7) ^ (rx & 7)) << 4); };
+      auto q_off = [&](int rx, int k) { return (rx / kRows) * Cfg::Q_BYTES + int(sw128_off(rx % kRows, k)); };
+      // (rows that do not exist are not loaded: their scores are not looked at)
+      const int rows = min(N, (w.ql * G - w.rb * N + 15) & ~15);
       if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
 #pragma unroll 1
-      for (int rx = r0; rx < N; rx += STEP) {
+      for (int rx = r0; rx < rows; rx += STEP) {
         const int ri = w.rb * N + rx, i = p.per_head(ri);
         const bool in = ri < w.ql * G;
         const size_t gr = in ? (size_t(w.b) * s.Nq + i) * p.H_q + w.h * G + (ri - i * G) : 0;
@@ -637,7 +627,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         copy_wait();
         bar_sync(1, PW * 32);                     // rows and fragments are there
 #pragma unroll 1
-        for (int rb = pw * 16; rb < N; rb += PW * 16) {
+        for (int rb = pw * 16; rb < rows; rb += PW * 16) {
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -682,7 +672,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         copy_wait();
       }
 #pragma unroll 1
-      for (int rx = r0; rx < N; rx += STEP) {
+      for (int rx = r0; rx < rows; rx += STEP) {
         uint4* at = reinterpret_cast<uint4*>(qt + q_off(rx, c));
         const uint4 v = *at;
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -694,7 +684,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         for (int o = LPR / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
         const float top = fmaxf(__uint_as_float(am << 16), s.r > 0 ? scr[rx] : 0.0f);
         const int e = top > 0.0f && top < INFINITY && am < 0x7f80u ? min(max(15 - exp_above(top), -126), 64) : 0;
-        const float qmul = pow2(e);
+        const float qmul = p.q_sign * pow2(e);
         uint32_t o4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -709,9 +699,9 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       if (s.r > 0) {
         bar_sync(1, PW * 32);                     // the rows' exponents are there
 #pragma unroll 1
-        for (int rb = pw * 16; rb < N; rb += PW * 16) {
-          uint8_t* ut = smem + Cfg::OFF_U;
-          const int ra = rb + (lane >> 2), q = (lane & 3) * 4;
+        for (int rb = pw * 16; rb < rows; rb += PW * 16) {
+          uint8_t* ut = smem + Cfg::OFF_U + (rb / kRows) * Cfg::U_BYTES;
+          const int ra = rb + (lane >> 2), rt = ra % kRows, q = (lane & 3) * 4;
           if constexpr (N > PW * 16) {
             const float* uf = reinterpret_cast<const float*>(smem + Cfg::OFF_UF) + rb * 16;
 #pragma unroll
@@ -722,11 +712,11 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
               acc[nt][0] = x.x; acc[nt][1] = x.y; acc[nt][2] = y.x; acc[nt][3] = y.y;
             }
           }
-          const float ma = pow2(qe[ra]), mb = pow2(qe[ra + 8]);
+          const float ma = p.q_sign * pow2(qe[ra]), mb = p.q_sign * pow2(qe[ra + 8]);
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
-            *reinterpret_cast<uint32_t*>(ut + nosw_off(ra, nt) + q) = pack_f16(acc[nt][0] * ma, acc[nt][1] * ma);
-            *reinterpret_cast<uint32_t*>(ut + nosw_off(ra + 8, nt) + q) = pack_f16(acc[nt][2] * mb, acc[nt][3] * mb);
+            *reinterpret_cast<uint32_t*>(ut + nosw_off(rt, nt) + q) = pack_f16(acc[nt][0] * ma, acc[nt][1] * ma);
+            *reinterpret_cast<uint32_t*>(ut + nosw_off(rt + 8, nt) + q) = pack_f16(acc[nt][2] * mb, acc[nt][3] * mb);
           }
         }
       }
@@ -776,7 +766,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
         const uint4* cent4 = reinterpret_cast<const uint4*>(s.cent) + size_t(w.h) * s.M * (D / 8) + part * (CH / 8);
         const int r = s.r, top = s.M - 1;
         const bool int8 = s.psac_fmt == 1, wide = s.M > 256;
-        constexpr int CP = 16 / TPR;              // PSAC coefficients of a thread
+        constexpr int CP = 8;              // PSAC coefficients of a thread
 #pragma unroll 1
         for (int jj = 0; jj < cnt; ++jj, ++t) {
           const bool have = (w.j + jj) * kKeys + row < w.len;
@@ -854,204 +844,193 @@ __global__ void __launch_bounds__(RCfg<D, NT>::kThreads, 1) rows_attn_kernel(con
       }
     }
   } else {
-    // ====== softmax of CPT columns (thread = key = TMEM lane) ======
+    // ================= softmax (thread = row = TMEM lane) =================
     set_regs<Cfg::kRegsSoft, Cfg::kRegs>();
-    const int g = warp >> 2, wq = warp & 3, kl = wq * 32 + lane, bid = 2 + g;
+    const int x = warp >> 2, wq = warp & 3, row = wq * 32 + lane, ru = (WIDE ? x * kRows : 0) + row;
     const uint32_t lane_base = uint32_t(wq * 32) << 16;
-    const uint32_t tO = tmem + 2 * N + g * CPT + lane_base;
-    float4* tab = reinterpret_cast<float4*>(smem + Cfg::OFF_TAB) + g * (CPT / 2);
-    float* tabf = reinterpret_cast<float*>(tab);
-    float* mrow = reinterpret_cast<float*>(smem + Cfg::OFF_MROW) + g * CPT;
-    float* alpha = reinterpret_cast<float*>(smem + Cfg::OFF_ALPHA) + g * CPT;
-    int* row_s = reinterpret_cast<int*>(smem + Cfg::OFF_ROW) + g * CPT;
-    float* red = reinterpret_cast<float*>(smem + Cfg::OFF_RED) + g * 4 * CPT;
-    auto wait_pv = [&](int tt) {                // P . V of tile tt is complete
-      return mbar_wait_or_abort(bar + B_PDONE + 8 * (tt % PB), (tt / PB) & 1, p.budget, abort);
-    };
-    float l[CPT];
-#pragma unroll
-    for (int c = 0; c < CPT; ++c) l[c] = 0.0f;
-    bool dead = false;                          // a wait ran out (seen by this thread)
-    bool gone = false;                          // ... by the group
-    int t = 0, seg = 0;
-    for (; w.more(); ++seg) {
+    const uint32_t tS = tmem + x * kKeys + lane_base, tO = tmem + 2 * kKeys + x * kRows + lane_base;
+    float2* ml_s = reinterpret_cast<float2*>(smem + Cfg::OFF_ML);
+    bool dead = false;                            // a wait ran out
+    int t0 = 0, seg = 0, k = 0;                   // the part's first tile; tiles of this group
+    for (; w.more(); w.next(p), ++seg) {
       const RowsSource& s = p.src[w.src];
-      const int cnt = w.count(), j0 = w.j, len = w.len, h = w.h;
-      const float* scr = reinterpret_cast<const float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N + g * CPT;
-      for (int jj = 0; jj < cnt && !gone; ++jj, ++t) {
-        const int sbuf = t & 1;
-        const uint32_t tS = tmem + sbuf * N + g * CPT + lane_base;
-        dead |= !mbar_wait_or_abort(bar + B_SFULL + 8 * sbuf, (t >> 1) & 1, p.budget, abort);
+      const int cnt = w.count(), j0 = w.j, len = w.len;
+      const int live = w.ql * G - w.rb * N;       // rows of the unit
+      const bool row_ok = ru < live, warp_ok = ru - lane < live;
+      const int jx = WIDE ? 0 : (x - t0) & 1;     // the group's first tile of the part
+      float m = -INFINITY, l = 0.0f, base = 0.0f, sc = 0.0f, nm = 0.0f;
+      for (int jj = jx; jj < cnt; jj += WIDE ? 1 : 2, ++k) {
+        dead |= !mbar_wait_or_abort(bar + B_SFULL + 8 * x, k & 1, p.budget, abort);
         fence_after_sync();
-        const int k0 = (j0 + jj) * kKeys;
-        const bool valid = k0 + kl < len, full = k0 + kKeys <= len;
-        uint8_t* pt8 = smem + Cfg::OFF_P + (t % PB) * Cfg::P_BYTES;
+        if (warp_ok) {
+          const bool first = jj == jx;
+          if (first) base = reinterpret_cast<const float*>(smem + Cfg::OFF_SCR)[(seg & 3) * N + ru];
+          const int lim = len - (j0 + jj) * kKeys;             // keys of the tile
+          const bool full = lim >= kKeys;
+          // the tile's maximum, 8 independent chains
+          float mp[8];
 #pragma unroll
-        for (int c0 = 0; c0 < CPT; c0 += 16) {
-          if (gone) break;
-          uint32_t pw[8];
-          bool checked = jj == 0, refresh = jj == 0;
+          for (int i = 0; i < 8; ++i) mp[i] = -INFINITY;
 #pragma unroll 1
-          for (;;) {
-            if (refresh) {
-              // new maxima for the rows whose scores pass the old ones by more than the margin
-              if (bar_or(bid, 128, dead)) {
-                gone = true;
-                break;
-              }
-              float v[16];
-              tmem_ld16(tS + c0, v);
-              int mine = 0;
+          for (int c0 = 0; c0 < kKeys; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32_issue(tS + c0, r);
+            tmem_wait_ld(r);
+            if (full) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float sv = valid ? v[i] * scr[c0 + i] : -INFINITY;
-                const int m = __reduce_max_sync(0xffffffffu, f2ord(sv));
-                if (lane == i) mine = m;
-              }
-              if (lane < 16) red[wq * CPT + c0 + lane] = ord2f(mine);
-              // O is rescaled below: P . V of the tile before must be complete
-              if (jj > 0) dead |= !wait_pv(t - 1);
-              fence_after_sync();
-              bar_sync(bid, 128);
-              if (kl < 16) {
-                const int c = c0 + kl;
-                const float tm = fmaxf(fmaxf(red[c], red[CPT + c]), fmaxf(red[2 * CPT + c], red[3 * CPT + c]));
-                // A whole number: every rescaling is by an exact power of two, and
-                // p's rounding does not depend on where the work is cut. Only the
-                // rows that need it: a row's result does not depend on the others.
-                const float mo = jj == 0 ? -INFINITY : mrow[c], mn = tm > mo + (kTrail - kBias) ? ceilf(tm) : mo;
-                alpha[c] = mn == -INFINITY ? 1.0f : ex2(mo - mn);
-                mrow[c] = mn;
-                // s sc - m is one fma, exact to half a step of m: beyond 2^20 (where
-                // a key's fp16 rounding already moves the score by 2^8) the row's
-                // scores are taken at a 2^-k of their size, so that this stays small
-                const float damp =
-                    fabsf(mn) > 0x1p20f && fabsf(mn) < INFINITY ? pow2(-max(exp_above(fabsf(mn)) - 21, 0)) : 1.0f;
-                tabf[(c >> 1) * 4 + (c & 1)] = scr[c] * damp;
-                tabf[(c >> 1) * 4 + 2 + (c & 1)] = mn == -INFINITY ? 0.0f : kBias - mn * damp;
-              }
-              bar_sync(bid, 128);
-              if (jj > 0) {
+              for (int i = 0; i < 32; i += 2)
+                mp[(i >> 1) & 7] = fmax3(mp[(i >> 1) & 7], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+            } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) l[c0 + i] *= alpha[c0 + i];
-                uint32_t o[16];
-                tmem_ld16(tO + c0, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(v[i] * alpha[c0 + i]);
-                tmem_st16(tO + c0, o);
-                tmem_wait_st();
-              }
-            }
-            float v[16], mx = -INFINITY;
-            tmem_ld16(tS + c0, v);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float4 k = tab[(c0 + i) >> 1];
-              const float2 xx = up2(ffma2(pk2(v[i], v[i + 1]), pk2(k.x, k.y), pk2(k.z, k.w)));
-              mx = fmax3(mx, xx.x, xx.y);
-              pw[i / 2] = pack_f16(ex2(xx.x), ex2(xx.y));
-            }
-            if (checked) break;
-            checked = true;
-            refresh = bar_or(bid, 128, (valid && mx > kTrail) || dead);
-            if (!refresh) break;
-          }
-          if (gone) break;
-          if (!full) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) pw[i] = valid ? pw[i] : 0u;
-          }
-          if (c0 + 16 == CPT) {                   // all scores are read: the buffer may be rewritten
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar + B_SFREE + 8 * sbuf);
-          }
-          // the sums of what enters P . V (the unit's first tile starts them)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (jj == 0) l[c0 + 2 * i] = l[c0 + 2 * i + 1] = 0.0f;
-            add_f16x2(l[c0 + 2 * i], l[c0 + 2 * i + 1], pw[i]);
-          }
-          if (c0 == 0 && t >= PB) dead |= !wait_pv(t - PB);    // the buffer is free
-          if constexpr (N >= 64) {
-            // rows along the operand's contiguous dimension: [N / 64][key][64 rows], swizzled
-            const int ck = (g * CPT + c0) / 8;
-            *reinterpret_cast<uint4*>(pt8 + sw128_off(kl, ck)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-            *reinterpret_cast<uint4*>(pt8 + sw128_off(kl, ck + 1)) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
-          } else {
-            // keys along the contiguous dimension: [2][row][64 keys], swizzled
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int rr = g * CPT + c0 + i;
-              *reinterpret_cast<uint16_t*>(pt8 + (kl >> 6) * N * 128 + rr * 128 + ((((kl & 63) >> 3) ^ (rr & 7)) << 4) +
-                                           (kl & 7) * 2) = uint16_t((i & 1) ? pw[i / 2] >> 16 : pw[i / 2] & 0xffffu);
+              for (int i = 0; i < 32; ++i)
+                if (c0 + i < lim) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(r[i]));
             }
           }
+          const float tm = base * fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                                        fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+          const bool up = tm > m + kTrail;
+          if (__any_sync(0xffffffffu, up)) {
+            // a row's maximum moves up: its sums follow (by an exact power of two)
+            const float mn = up ? ceilf(tm) : m;
+            const float alpha = up ? ex2(m - mn) : 1.0f;       // (m = -inf: 0, nothing summed yet)
+            m = mn;
+            l *= alpha;
+            if (up) {
+              // s sc - m is one fma, exact to half a step of m: beyond 2^20 (where a
+              // key's fp16 rounding already moves the score by 2^8) the row's scores
+              // are taken at a 2^-i of their size, so that this stays small
+              const float damp =
+                  fabsf(mn) > 0x1p20f && fabsf(mn) < INFINITY ? pow2(-max(exp_above(fabsf(mn)) - 21, 0)) : 1.0f;
+              sc = base * damp;
+              nm = kBias - mn * damp;
+            }
+            if (!first) {                         // (the scores came after P . V of the group's tile before)
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t r[32];
+                float v[32];
+                tmem_ld32_issue(tO + c0, r);
+                tmem_wait_ld(r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * alpha;
+                tmem_st32(tO + c0, v);
+              }
+            }
+          }
+          const f32x2 sc2 = pk2(sc, sc), nm2 = pk2(nm, nm);
+          f32x2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += 32) {
+            uint32_t r[32], pw[16];
+            tmem_ld32_issue(tS + c0, r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = up2(ffma2(pk2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sc2, nm2));
+              float p0 = ex2(y.x), p1 = ex2(y.y);
+              if (!full) {
+                p0 = c0 + i < lim ? p0 : 0.0f;
+                p1 = c0 + i + 1 < lim ? p1 : 0.0f;
+              }
+              sum[(i >> 1) & 3] = fadd2(sum[(i >> 1) & 3], pk2(p0, p1));
+              pw[i / 2] = pack_f16(p0, p1);
+            }
+            tmem_st16(tS + c0 / 2, pw);           // over columns already read
+          }
+          tmem_wait_st();
+          const float2 s01 = up2(fadd2(sum[0], sum[1])), s23 = up2(fadd2(sum[2], sum[3]));
+          l += (s01.x + s23.x) + (s01.y + s23.y);
         }
-        if (gone) break;
-        fence_proxy_async();
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar + B_PFULL + 8 * (t % PB));
+        if (lane == 0) mbar_arrive(bar + B_PFULL + 8 * x);
       }
-      // ---- the unit's rows
-      if (!gone) {
-        dead |= !wait_pv(t - 1);
-        fence_after_sync();
-        gone = bar_or(bid, 128, dead);
+      // ---- the unit's rows: a group's 128 rows, or half their channels of both groups' sums
+      if (jx < cnt) dead |= !mbar_wait_or_abort(bar + B_PDONE + 8 * x, (k - 1) & 1, p.budget, abort);
+      fence_after_sync();
+      float f0 = 1.0f, f1 = 0.0f;
+      if constexpr (!WIDE) {
+        ml_s[x * kRows + row] = make_float2(m, l);
+        dead = bar_or(2, 256, dead);
+        fence_after_sync();                       // the other group's sums too
+        const float2 a = ml_s[row], b = ml_s[kRows + row];
+        m = fmaxf(a.y == 0.0f ? -INFINITY : a.x, b.y == 0.0f ? -INFINITY : b.x);
+        f0 = a.y == 0.0f ? 0.0f : ex2(a.x - m);
+        f1 = b.y == 0.0f ? 0.0f : ex2(b.x - m);
+        l = f0 * a.y + f1 * b.y;
       }
-      warp_colsum<CPT>(l, lane);
-      if (lane < CPT) red[wq * CPT + lane] = l[0];
-      bar_sync(bid, 128);
       const bool whole = j0 == 0 && cnt == tiles_of(len);
-      const int slot = j0 > 0 ? 0 : 1;
-      const int r0 = w.rb * N + g * CPT, live = min(CPT, w.ql * G - r0);
-      if (kl < CPT) {
-        float lt = (red[kl] + red[CPT + kl]) + (red[2 * CPT + kl] + red[3 * CPT + kl]);
-        float m = mrow[kl];
-        if (gone) {
-          lt = 1.0f;
-          m = 0.0f;
-        }
-        alpha[kl] = lt > 0.0f ? 1.0f / lt : (lt == 0.0f ? 0.0f : lt);
-        if (kl < live) {
-          // row of (sequence, query, head) in Q and out
-          const int ri = r0 + kl, i = p.per_head(ri), row = (w.b * s.Nq + i) * p.H_q + h * G + (ri - i * G);
-          row_s[kl] = row;
-          if (!whole) p.part_ml[(size_t(blockIdx.x) * 2 + slot) * N + g * CPT + kl] = make_float2(m, lt);
-          else if (!p.out) p.dir_ml[size_t(w.src) * p.dir_rows + row] = make_float2(m, lt);
-        }
+      if (dead) {
+        m = 0.0f;
+        l = 1.0f;
       }
-      bar_sync(bid, 128);
-#pragma unroll 1
-      for (int c0 = 0; c0 < CPT; c0 += 16) {
-        if (c0 >= live) break;
-        float v[16];
-        if (!gone) {
-          tmem_ld16(tO + c0, v);                  // every lane: warp-wide TMEM load
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __int_as_float(0x7fc00000);
+      if (warp_ok) {
+        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+        const int ri = w.rb * N + ru, i = p.per_head(ri);
+        const size_t gr = (size_t(w.b) * s.Nq + i) * p.H_q + w.h * G + (ri - i * G);
+        const size_t pr = (size_t(blockIdx.x) * 2 + (j0 > 0 ? 0 : 1)) * N + ru;
+        float* po = !whole ? p.part_o + pr * D : p.dir_o + (size_t(w.src) * p.dir_rows + gr) * D;
+        if (row_ok && (WIDE || x == 0)) {
+          if (!whole) p.part_ml[pr] = make_float2(m, l);
+          else if (!p.out) p.dir_ml[size_t(w.src) * p.dir_rows + gr] = make_float2(m, l);
         }
-        if (kl < D) {
+        const int c_lo = WIDE ? 0 : x * (D / 2), c_hi = WIDE ? D : c_lo + D / 2;
+        const bool has0 = !WIDE && (cnt > 1 || (t0 & 1) == 0), has1 = !WIDE && (cnt > 1 || (t0 & 1) == 1);
+#pragma unroll 1
+        for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+          float v[32];
+          uint32_t r[32];
+          if constexpr (WIDE) {
+            tmem_ld32_issue(tO + c0, r);          // every lane: warp-wide TMEM load
+            tmem_wait_ld(r);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = c0 + i;
-            if (c >= live) break;
-            if (!whole) {
-              p.part_o[((size_t(blockIdx.x) * 2 + slot) * N + g * CPT + c) * D + kl] = v[i];
-            } else if (!p.out) {
-              p.dir_o[(size_t(w.src) * p.dir_rows + row_s[c]) * D + kl] = v[i];
-            } else {
-              const float o = v[i] * alpha[c];
-              const size_t at = size_t(row_s[c]) * D + kl;
-              if (p.out_dtype == KV2_OUT_F32) static_cast<float*>(p.out)[at] = o;
-              else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
+            for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
+          } else {
+            const uint32_t tB = tmem + 2 * kKeys + lane_base + c0;
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = 0.0f;
+            if (has0) {
+              tmem_ld32_issue(tB, r);
+              tmem_wait_ld(r);
+              if (f0 != 0.0f) {
+#pragma unroll
+                for (int q = 0; q < 32; ++q) v[q] = f0 * __uint_as_float(r[q]);
+              }
             }
+            if (has1) {
+              tmem_ld32_issue(tB + kRows, r);
+              tmem_wait_ld(r);
+              if (f1 != 0.0f) {
+#pragma unroll
+                for (int q = 0; q < 32; ++q) v[q] = fmaf(f1, __uint_as_float(r[q]), v[q]);
+              }
+            }
+          }
+          if (dead) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = __int_as_float(0x7fc00000);
+          }
+          if (!row_ok) continue;
+          if (!whole || !p.out) {
+            float4* dst = reinterpret_cast<float4*>(po + c0);
+#pragma unroll
+            for (int q = 0; q < 32; q += 4) dst[q / 4] = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+          } else if (p.out_dtype == KV2_OUT_F32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + gr * D + c0);
+#pragma unroll
+            for (int q = 0; q < 32; q += 4) dst[q / 4] = make_float4(v[q] * inv, v[q + 1] * inv, v[q + 2] * inv, v[q + 3] * inv);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + gr * D + c0);
+#pragma unroll
+            for (int q = 0; q < 32; q += 8)
+              dst[q / 8] = make_uint4(pack_bf16(v[q] * inv, v[q + 1] * inv), pack_bf16(v[q + 2] * inv, v[q + 3] * inv),
+                                      pack_bf16(v[q + 4] * inv, v[q + 5] * inv), pack_bf16(v[q + 6] * inv, v[q + 7] * inv));
           }
         }
       }
-      w.next(p);
+      // both groups' sums are read before the next unit's P . V starts them afresh
+      if constexpr (!WIDE) bar_sync(2, 256);
+      t0 += cnt;
     }
   }
 
@@ -1205,7 +1184,7 @@ int sm_count() {
 }
 
 // rows per unit for the most rows that read the same keys
-int unit_rows(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int unit_rows(long long rows) { return rows <= kRows ? kRows : 2 * kRows; }
 
 // workspace: header (word 0 the error word, the tile count at byte 16), the
 // first tile of every sequence, the CTAs' places, pieces, whole units
@@ -1242,10 +1221,10 @@ RowsPlan plan_rows(const RowsArgs& a) {
   return pl;
 }
 
-template <int D, int N>
+template <int D, bool WIDE>
 cudaError_t launch_cfg(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) {
-  using Cfg = RCfg<D, N>;
-  auto kern = rows_attn_kernel<D, N>;
+  using Cfg = RCfg<D, WIDE>;
+  auto kern = rows_attn_kernel<D, WIDE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg::SMEM));
   if (e != cudaSuccess) return e;
   // the role split spends exactly these registers: with fewer at launch it would wait for ever
@@ -1272,12 +1251,7 @@ cudaError_t launch_cfg(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) 
 
 template <int D>
 cudaError_t launch_d(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) {
-  switch (pl.N) {
-    case 16: return launch_cfg<D, 16>(p, pl, s);
-    case 32: return launch_cfg<D, 32>(p, pl, s);
-    case 64: return launch_cfg<D, 64>(p, pl, s);
-    default: return launch_cfg<D, 128>(p, pl, s);
-  }
+  return pl.N == kRows ? launch_cfg<D, false>(p, pl, s) : launch_cfg<D, true>(p, pl, s);
 }
 
 }  // namespace
@@ -1311,7 +1285,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
   p.Q = a.Q;
   p.out = a.out;
   p.out_dtype = a.out_dtype;
-  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.scale_log2 = fabsf(a.sm_scale) * 1.4426950408889634f;
+  p.q_sign = a.sm_scale < 0.0f ? -1.0f : 1.0f;
   p.err = reinterpret_cast<int*>(ws);
   p.total = reinterpret_cast<long long*>(ws + 16);
   p.base = reinterpret_cast<long long*>(ws + pl.base);
