@@ -444,12 +444,24 @@ kv2::RowsArgs shared_args(const kv2_cache* pre, const int32_t* prefix_lens, int 
   return a;
 }
 
+// One query per sequence whose group the decode kernel is built for goes to it:
+// its four CTAs an SM hide each other's latencies, where the row kernel's one
+// CTA spends them on four busy rows (1,500 tokens x 16 x 8 heads: 46 us there).
+bool cross_is_decode(const kv2_cache* c, int H_q, int Nq) {
+  const int G = H_q / c->H_kv;
+  return Nq == 1 && (G == 1 || G == 2 || G == 4 || G == 8);
+}
+size_t cross_workspace(const kv2_cache* c, int H_q, int Nq, int max_len) {
+  return cross_is_decode(c, H_q, Nq) ? kv2::decode_workspace_bytes(*c, H_q, max_len)
+                                     : kv2::rows_workspace_bytes(cross_args(c, nullptr, max_len, nullptr, Nq, H_q));
+}
+
 }  // namespace
 
 size_t kv2_attention_cross_workspace_size(const kv2_cache* c, int H_q, int Nq, int max_len) {
   if (!c || H_q <= 0 || c->H_kv <= 0 || H_q % c->H_kv || Nq < 0 || max_len < 0) return 0;
   if (check_cache(c, false, false) != KV2_OK || rows_too_many(c, H_q, Nq)) return 0;
-  return kv2::rows_workspace_bytes(cross_args(c, nullptr, max_len, nullptr, Nq, H_q));
+  return cross_workspace(c, H_q, Nq, max_len);
 }
 
 kv2_status kv2_attention_cross(const kv2_cache* c, const int32_t* lens, int max_len, const uint16_t* Q,
@@ -463,8 +475,14 @@ kv2_status kv2_attention_cross(const kv2_cache* c, const int32_t* lens, int max_
   if (rows_too_many(c, H_q, Nq)) return fail(KV2_ERR_UNSUPPORTED, "cross: %d x Nq=%d x H_q=%d rows above 2^30", c->B, Nq, H_q);
   if (Nq == 0) return ok();
   kv2::RowsArgs a = cross_args(c, lens, max_len, q_lens, Nq, H_q);
-  st = check_rows_io("cross", Q, out, out_dtype, ws, ws_bytes, kv2::rows_workspace_bytes(a));
+  st = check_rows_io("cross", Q, out, out_dtype, ws, ws_bytes, cross_workspace(c, H_q, Nq, max_len));
   if (st != KV2_OK) return st;
+  if (cross_is_decode(c, H_q, Nq)) {
+    kv2::DecodeArgs d{c, max_len, H_q, Q, sm_scale, out, out_dtype, ws, ws_bytes};
+    d.lens = lens;
+    d.q_lens = q_lens;
+    return cuda_status(kv2::launch_decode(d, static_cast<cudaStream_t>(stream)), "cross launch");
+  }
   a.Q = Q;
   a.sm_scale = sm_scale;
   a.out = out;

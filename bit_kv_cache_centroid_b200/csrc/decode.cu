@@ -13,12 +13,13 @@ using namespace dsplit;
 
 // ---------------------------------------------------------------------------
 __global__ void decode_combine(const float* __restrict__ part, int H_q, int H_kv, int D,
-                               int splits, void* out, int out_dtype) {
+                               int splits, void* out, int out_dtype, const int32_t* q_lens) {
   // launched as the split kernel's programmatic dependent: its partials are
   // complete and visible after this wait
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int bq = blockIdx.x;
   const int b = bq / H_q, hq = bq % H_q;
+  if (q_lens && q_lens[b] <= 0) return;              // the sequence has no query: its rows stay as they are
   const int G = H_q / H_kv, h = hq / G, g = hq % G;
   const float* base = part + (size_t(b * H_kv + h) * splits) * G * (D + 2) + g * (D + 2);
   const size_t sstride = size_t(G) * (D + 2);
@@ -130,7 +131,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
                  a.sm_scale * kLog2e, part, static_cast<int*>(a.ws),
                  force ? (1ull << 20) : env_wait_budget(), force, a.wait_from,
                  c.H_kv, a.H_q, c.M, c.r, c.capacity, a.len, splits, tps, c.psac_fmt, c.psac_scale,
-                 c.block_table, c.page_tokens};
+                 c.block_table, c.page_tokens, a.lens};
   const int G = a.H_q / c.H_kv;
   cudaError_t e;
   switch (cache_group(c)) {
@@ -152,7 +153,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, decode_combine, static_cast<const float*>(part), a.H_q, c.H_kv, c.d, splits,
-                            a.out, a.out_dtype);
+                            a.out, a.out_dtype, a.q_lens);
 }
 
 }  // namespace kv2

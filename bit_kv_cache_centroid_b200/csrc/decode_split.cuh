@@ -82,6 +82,7 @@ struct SplitParams {
   const uint16_t* psac_scale;
   const int32_t* table;         // paged cache: block table [B][cap / page] (null: contiguous)
   int page;
+  const int32_t* lens;          // tokens per sequence, device [B], taken into 0..len (null: len each)
 };
 
 // d = a * b + c on two fp16 lanes
@@ -279,8 +280,17 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
   const int b = bh / p.H_kv, h = bh % p.H_kv;
   const size_t base_slot = size_t(bh) * p.cap;
   const int t_begin = split * p.tiles_per_split * kTile;
-  const int t_end = min(p.len, t_begin + p.tiles_per_split * kTile);
+  const int len = p.lens ? min(max(p.lens[b], 0), p.len) : p.len;
+  const int t_end = min(len, t_begin + p.tiles_per_split * kTile);
   const int ntiles = (t_end > t_begin) ? (t_end - t_begin + kTile - 1) / kTile : 0;
+
+  if (p.lens && ntiles == 0) {
+    // a split behind its sequence's end: nothing to merge
+    asm volatile("griddepcontrol.launch_dependents;");
+    float* dst = p.part + (size_t(bh) * p.splits + split) * G * (D + 2);
+    for (int i = tid; i < G * (D + 2); i += kThreads) dst[i] = i % (D + 2) == D ? -FLT_MAX : 0.0f;
+    return;
+  }
 
   // tile copies: thread 0 issues one bulk copy per stream into the tile's
   // stage; they complete on the stage's barrier
