@@ -120,11 +120,16 @@ size_t decode_workspace_bytes(const kv2_cache& c, int H_q, int len) {
   return kWsHeader + size_t(c.B) * c.H_kv * splits * (H_q / c.H_kv) * (c.d + 2) * 4;
 }
 
-cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
+int decode_splits(const kv2_cache& c, int H_q, int len) {
+  int splits, tps;
+  plan_splits(c, H_q, len, &splits, &tps);
+  return splits;
+}
+
+cudaError_t launch_decode_split(const DecodeArgs& a, float* part, cudaStream_t s) {
   const kv2_cache& c = *a.c;
   int splits, tps;
   plan_splits(c, a.H_q, a.len, &splits, &tps);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kWsHeader);
   const int force = env_force_timeout();
   SplitParams sp{c.k_code, c.v_code, c.k_sz, c.v_sz, c.cidx, c.psac,
                  static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(c.centroids), c.P,
@@ -133,13 +138,19 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
                  c.H_kv, a.H_q, c.M, c.r, c.capacity, a.len, splits, tps, c.psac_fmt, c.psac_scale,
                  c.block_table, c.page_tokens, a.lens};
   const int G = a.H_q / c.H_kv;
-  cudaError_t e;
   switch (cache_group(c)) {
-    case 32: e = launch_gs<32>(c, G, sp, s); break;
-    case 64: e = launch_gs<64>(c, G, sp, s); break;
-    case 128: e = launch_gs<128>(c, G, sp, s); break;
-    default: e = cudaErrorInvalidValue;
+    case 32: return launch_gs<32>(c, G, sp, s);
+    case 64: return launch_gs<64>(c, G, sp, s);
+    case 128: return launch_gs<128>(c, G, sp, s);
+    default: return cudaErrorInvalidValue;
   }
+}
+
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
+  const kv2_cache& c = *a.c;
+  const int splits = decode_splits(c, a.H_q, a.len);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kWsHeader);
+  const cudaError_t e = launch_decode_split(a, part, s);
   if (e != cudaSuccess) return e;
   // the merge runs as the split kernel's programmatic dependent (its launch
   // overlaps the split kernel's last CTAs)

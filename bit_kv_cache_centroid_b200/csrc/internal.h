@@ -121,6 +121,11 @@ struct DecodeArgs {
 };
 size_t decode_workspace_bytes(const kv2_cache& c, int H_q, int len);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
+// Its first kernel alone: per (sequence, KV head), split and query head of the
+// group, d unnormalised sums, the running maximum (log2 units) and the softmax
+// denominator, [B * H_kv][splits][G][d + 2].
+int decode_splits(const kv2_cache& c, int H_q, int len);
+cudaError_t launch_decode_split(const DecodeArgs& a, float* part, cudaStream_t s);
 
 // PSAC basis fit.
 struct FitArgs {

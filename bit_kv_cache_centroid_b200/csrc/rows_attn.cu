@@ -108,6 +108,8 @@ struct RowsParams {
   float* dir_o;             // whole units [source][rows][D]
   float2* dir_ml;
   long long dir_rows;       // rows per source of dir_*
+  const float* split_part;  // the second source's results from the split decode kernel (null: from this one)
+  int splits;
   unsigned long long budget;
   int force_timeout;
 };
@@ -971,8 +973,9 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
         const size_t pr = (size_t(blockIdx.x) * 2 + (j0 > 0 ? 0 : 1)) * N + ru;
         float* po = !whole ? p.part_o + pr * D : p.dir_o + (size_t(w.src) * p.dir_rows + gr) * D;
         if (row_ok && (WIDE || x == 0)) {
-          if (!whole) p.part_ml[pr] = make_float2(m, l);
-          else if (!p.out) p.dir_ml[size_t(w.src) * p.dir_rows + gr] = make_float2(m, l);
+          // (sums carry 2^kBias: the stored maximum takes it out)
+          if (!whole) p.part_ml[pr] = make_float2(m - kBias, l);
+          else if (!p.out) p.dir_ml[size_t(w.src) * p.dir_rows + gr] = make_float2(m - kBias, l);
         }
         const int c_lo = WIDE ? 0 : x * (D / 2), c_hi = WIDE ? D : c_lo + D / 2;
         const bool has0 = !WIDE && (cnt > 1 || (t0 & 1) == 0), has1 = !WIDE && (cnt > 1 || (t0 & 1) == 1);
@@ -1035,8 +1038,10 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
   }
 
   // the merge (this grid's programmatic dependent) may be scheduled; it waits
-  // for this grid before it reads anything
+  // for this grid before it reads anything, and so, through this wait, for the
+  // split decode kernel that this grid may have been launched beside
   asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   fence_before_sync();
   __syncthreads();
   if (warp == Cfg::kMmaWarp) {
@@ -1145,8 +1150,43 @@ __global__ void __launch_bounds__(256) rows_merge_shared(const __grid_constant__
   const int G = p.H_q / p.H_kv, hq = int(gr % p.H_q), h = hq / G, g = hq % G;
   const long long T = *p.total;
   float m[2], l[2], o[2][D / 32];
+  if (p.split_part) {
+    // own cache: lane s of the warp weighs split s (32 at a time)
+    const float* base = p.split_part + (gr / p.H_q * p.H_kv + h) * size_t(p.splits) * G * (D + 2) + size_t(g) * (D + 2);
+    const size_t step = size_t(G) * (D + 2);
+    float top = -INFINITY;
+    for (int s0 = lane; s0 < p.splits; s0 += 32)
+      if (base[s0 * step + D + 1] != 0.0f) top = fmaxf(top, base[s0 * step + D]);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    m[1] = top;
+    l[1] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) o[1][k] = 0.0f;
+    for (int s0 = 0; s0 < p.splits; s0 += 32) {
+      float f = 0.0f;
+      if (s0 + lane < p.splits) {
+        const float ls = base[(s0 + lane) * step + D + 1];
+        if (ls != 0.0f) {
+          f = exp2f(base[(s0 + lane) * step + D] - top);
+          l[1] = fmaf(f, ls, l[1]);
+        }
+      }
+      const int n = min(32, p.splits - s0);
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float fj = __shfl_sync(0xffffffffu, f, j);
+        if (fj == 0.0f) continue;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) o[1][k] = fmaf(fj, base[(s0 + j) * step + k * 32 + lane], o[1][k]);
+      }
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
+  }
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
+    if (s == 1 && p.split_part) break;
     const RowsSource& src = p.src[s];
     const int seq = int(gr / p.H_q), b = seq / src.Nq, i = seq % src.Nq;
     const int nb = tiles_of(seq_len(src, b)), RB = blocks_of<N>(src.Nq, G);
@@ -1189,21 +1229,30 @@ int unit_rows(long long rows) { return rows <= kRows ? kRows : 2 * kRows; }
 // workspace: header (word 0 the error word, the tile count at byte 16), the
 // first tile of every sequence, the CTAs' places, pieces, whole units
 struct RowsPlan {
-  int N, C;
+  int N, C, listed, splits;   // sources in the work list; splits of the own caches by the decode kernel (0: listed)
   long long rows;
-  size_t base, cta, part_ml, part_o, dir_ml, dir_o, bytes;
+  size_t base, cta, part_ml, part_o, dir_ml, dir_o, split, bytes;
 };
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 RowsPlan plan_rows(const RowsArgs& a) {
   RowsPlan pl{};
   const int G = a.H_q / a.src[0].c->H_kv, d = a.src[0].c->d;
+  // The sequences' own caches have G rows a unit. With more such units than SMs
+  // the split decode kernel, where it is built for them, takes them sooner (64
+  // sequences x 8 heads of up to 515 tokens behind a 32,768-token prefix: 133 us
+  // against 200 us); with fewer its launch costs more than they do in the list
+  // (8 x 8 of up to 256: 82 against 75 us).
+  const bool by_decode = a.nsrc == 2 && (G == 1 || G == 2 || G == 4 || G == 8) &&
+                         static_cast<long long>(a.src[1].c->B) * a.src[1].c->H_kv > sm_count();
+  pl.listed = by_decode ? 1 : a.nsrc;
+  if (pl.listed < a.nsrc) pl.splits = decode_splits(*a.src[1].c, a.H_q, a.src[1].max_len);
   long long most = 0;
-  for (int s = 0; s < a.nsrc; ++s) most = std::max(most, static_cast<long long>(a.src[s].Nq) * G);
+  for (int s = 0; s < pl.listed; ++s) most = std::max(most, static_cast<long long>(a.src[s].Nq) * G);
   pl.N = unit_rows(most);
   long long tiles = 0;
   size_t seqs = 0;
-  for (int s = 0; s < a.nsrc; ++s) {
+  for (int s = 0; s < pl.listed; ++s) {
     const long long rows = static_cast<long long>(a.src[s].Nq) * G;
     tiles += static_cast<long long>(std::max(1, (a.src[s].max_len + kKeys - 1) / kKeys)) * ((rows + pl.N - 1) / pl.N) *
              a.src[s].c->H_kv * a.src[s].c->B;
@@ -1216,8 +1265,9 @@ RowsPlan plan_rows(const RowsArgs& a) {
   pl.part_ml = pl.cta + up256(size_t(pl.C) * 16);
   pl.part_o = pl.part_ml + up256(size_t(pl.C) * 2 * pl.N * 8);
   pl.dir_ml = pl.part_o + up256(size_t(pl.C) * 2 * pl.N * d * 4);
-  pl.dir_o = pl.dir_ml + (a.nsrc == 2 ? up256(size_t(2) * pl.rows * 8) : 0);
-  pl.bytes = pl.dir_o + (a.nsrc == 2 ? up256(size_t(2) * pl.rows * d * 4) : 0);
+  pl.dir_o = pl.dir_ml + (a.nsrc == 2 ? up256(size_t(pl.listed) * pl.rows * 8) : 0);
+  pl.split = pl.dir_o + (a.nsrc == 2 ? up256(size_t(pl.listed) * pl.rows * d * 4) : 0);
+  pl.bytes = pl.split + size_t(a.src[0].c->H_kv) * (a.nsrc == 2 ? a.src[1].c->B : 0) * pl.splits * G * (d + 2) * 4;
   return pl;
 }
 
@@ -1232,21 +1282,30 @@ cudaError_t launch_cfg(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) 
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != Cfg::kRegs) return cudaErrorInvalidConfiguration;
+  const bool both = p.dir_o != nullptr;       // a shared prefix: rows are joined by the merge
   RowsParams q = p;
-  if (p.nsrc == 2) q.out = nullptr;
-  kern<<<pl.C, Cfg::kThreads, Cfg::SMEM, s>>>(q);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || (p.nsrc == 1 && pl.C == 1)) return e;
+  if (both) q.out = nullptr;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = p.nsrc == 2 ? dim3(unsigned((pl.rows + 7) / 8)) : dim3(pl.C - 1, Cfg::N / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(pl.C);
+  cfg.blockDim = dim3(Cfg::kThreads);
+  cfg.dynamicSmemBytes = Cfg::SMEM;
+  cfg.stream = s;
+  if (pl.splits) {                            // beside the last blocks of the split decode kernel
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  e = cudaLaunchKernelEx(&cfg, kern, q);
+  if (e != cudaSuccess || (!both && pl.C == 1)) return e;
+  cfg = cudaLaunchConfig_t{};
+  cfg.gridDim = both ? dim3(unsigned((pl.rows + 7) / 8)) : dim3(pl.C - 1, Cfg::N / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, p.nsrc == 2 ? rows_merge_shared<D, Cfg::N> : rows_merge_cut<D, Cfg::N>, p, pl.C);
+  return cudaLaunchKernelEx(&cfg, both ? rows_merge_shared<D, Cfg::N> : rows_merge_cut<D, Cfg::N>, p, pl.C);
 }
 
 template <int D>
@@ -1277,7 +1336,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
     q.Nq = a.src[i].Nq;
   }
   char* ws = static_cast<char*>(a.ws);
-  p.nsrc = a.nsrc;
+  p.nsrc = pl.listed;
   p.H_kv = a.src[0].c->H_kv;
   p.H_q = a.H_q;
   const uint32_t G = uint32_t(a.H_q / p.H_kv);
@@ -1294,8 +1353,17 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
   p.dir_ml = reinterpret_cast<float2*>(ws + pl.dir_ml);
-  p.dir_o = reinterpret_cast<float*>(ws + pl.dir_o);
+  p.dir_o = a.nsrc == 2 ? reinterpret_cast<float*>(ws + pl.dir_o) : nullptr;
   p.dir_rows = pl.rows;
+  if (pl.splits) {
+    float* part = reinterpret_cast<float*>(ws + pl.split);
+    DecodeArgs d{a.src[1].c, a.src[1].max_len, a.H_q, a.Q, a.sm_scale, nullptr, a.out_dtype, a.ws, 0};
+    d.lens = a.src[1].lens;
+    p.split_part = part;
+    p.splits = pl.splits;
+    const cudaError_t e = launch_decode_split(d, part, s);
+    if (e != cudaSuccess) return e;
+  }
   p.force_timeout = env_force_timeout();
   p.budget = p.force_timeout ? (1ull << 20) : env_wait_budget();
   return a.src[0].c->d == 64 ? launch_d<64>(p, pl, s) : launch_d<128>(p, pl, s);

@@ -134,6 +134,10 @@ SHARED = [
     (3, 11, 1, 3, 64, (16, 16, 1, 64, 0), (16, 0, 0, 32, 128), [1, 640, 127], [1 + 7 * k for k in range(33)], 1),
     (1, 40, 2, 4, 128, (64, 8, 0, 64, 0), (64, 8, 0, 64, 0), [1500], [3 * k for k in range(40)], 0),
     (2, 1, 2, 1, 64, (8, 8, 0, 32, 0), (8, 8, 0, 32, 0), [0, 40], [0, 0], 0),
+    # more own caches than SMs: their part by the split decode kernel
+    (3, 31, 2, 2, 128, (64, 8, 0, 32, 0), (64, 8, 1, 32, 128), [200, 0, 513], [(7 * k) % 400 for k in range(93)], 1),
+    (1, 160, 1, 8, 64, (16, 16, 0, 32, 0), (300, 8, 0, 64, 0), [300], [(11 * k) % 260 for k in range(160)], 0),
+    (2, 90, 1, 3, 64, (16, 0, 0, 32, 0), (16, 0, 0, 32, 0), [64, 300], [(5 * k) % 200 for k in range(180)], 0),
 ]
 
 
