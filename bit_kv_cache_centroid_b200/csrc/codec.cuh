@@ -84,4 +84,47 @@ __device__ __forceinline__ GroupParams code_values(const uint16_t* vrow, uint32_
   return gp;
 }
 
+// The same codes by GS / 8 consecutive lanes, 8 values each: returns this
+// lane's 16 bits of the code words. The minimum, the maximum and the choice of
+// each code are those of code_values, whatever lanes share them. Lanes move 16
+// contiguous bytes and hold 8 values, a quarter of code_values' registers.
+template <int GS>
+__device__ __forceinline__ GroupParams code_values8(const uint4 vv, uint32_t& bits) {
+  const uint32_t vu[4] = {vv.x, vv.y, vv.z, vv.w};
+  float x[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    x[2 * q] = __uint_as_float(vu[q] << 16);
+    x[2 * q + 1] = __uint_as_float(vu[q] & 0xffff0000u);
+  }
+  float mn = fminf(fmin3(x[0], x[1], x[2]), fmin3(x[3], x[4], x[5])), mx = fmaxf(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]));
+  mn = fmin3(mn, x[6], x[7]);
+  mx = fmax3(mx, x[6], x[7]);
+#pragma unroll
+  for (int o = 1; o < GS / 8; o <<= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  const GroupParams gp = group_params(mn, mx);
+  const float inv_s = __frcp_rn(gp.s);
+  uint32_t redo = 0;
+  bits = 0;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float q = __fmul_rn(__fsub_rn(x[c], gp.z), inv_s), r = rintf(q);
+    bits |= uint32_t(fminf(fmaxf(r, 0.0f), 3.0f)) << (2 * c);
+    redo |= uint32_t(fabsf(__fsub_rn(q, r)) > 0.5f - 0x1p-18f) << c;
+  }
+  // the rare channels whose code the correctly rounded division decides
+#pragma unroll 1
+  for (; redo; redo &= redo - 1) {
+    const int c = __ffs(redo) - 1;
+    const uint32_t w = c < 4 ? (c < 2 ? vu[0] : vu[1]) : (c < 6 ? vu[2] : vu[3]);
+    const uint32_t q = group_code(__uint_as_float(c & 1 ? w & 0xffff0000u : w << 16), gp);
+    bits = (bits & ~(3u << (2 * c))) | (q << (2 * c));
+  }
+  if (gp.s == 0.0f) bits = 0;
+  return gp;
+}
+
 }  // namespace kv2

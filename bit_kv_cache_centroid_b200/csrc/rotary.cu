@@ -16,7 +16,13 @@
 //
 // Bound: memory; per token and KV head 256 B of key read, 256 B written and
 // read back (L2 for appends below its size), 256 B of values read, and per
-// query head 512 B (d = 128).
+// query head 512 B (d = 128). A token's chain of reads (count, place, page,
+// angles, rows) is long and its bytes few, so that many small blocks hide it
+// best: D / 8 lanes take a head row, each its 8 channels of every head with
+// the angles in registers, which leaves 32 registers a thread and 8 blocks an
+// SM. Measured against 48 registers (5 blocks), 2 or 4 heads' loads in flight
+// and several tokens a block: 75 us the append of up to 6 x 777 tokens (8 KV,
+// 32 query heads) against 77 to 90, of which the key kernel takes 50.
 #include "codec.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -39,93 +45,64 @@ struct RotateParams {
   int* err;
 };
 
-__device__ __forceinline__ float bf(uint32_t bits) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ float bf(uint32_t bits) { return __uint_as_float(bits << 16); }   // the low half
 __device__ __forceinline__ uint16_t bf_rn(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 __device__ __forceinline__ void turn(float a, float b, float c, float s, float& x, float& y) {
   x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
   y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return uint32_t(bf_rn(a)) | (uint32_t(bf_rn(b)) << 16);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-  v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+// two turned pairs of bf16: (a, b) in, (a', b') out
+__device__ __forceinline__ void turn2(uint32_t& a, uint32_t& b, float2 c, float2 n) {
+  float x0, y0, x1, y1;
+  turn(bf(a), bf(b), c.x, n.x, x0, y0);
+  turn(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u), c.y, n.y, x1, y1);
+  const __nv_bfloat162 p = __floats2bfloat162_rn(x0, x1), q = __floats2bfloat162_rn(y0, y1);
+  a = *reinterpret_cast<const uint32_t*>(&p);
+  b = *reinterpret_cast<const uint32_t*>(&q);
 }
 
-// One head row of D channels: task i of `tasks(rot)`. A task reads all it
-// writes before writing, so dst may be src.
-//   rot a multiple of 16, halves: chunks of 8 pairs, then chunks of 8 plain channels
-//   rot a multiple of 16, neighbours: chunks of 8 channels
-//   else: single pairs, then single plain channels
-template <int D>
-struct RowTurn {
-  const float* cs;      // the position's row: rot/2 cosines, rot/2 sines
-  int rot, inter;
-  __device__ int tasks() const {
-    if (rot & 15) return D - rot / 2;
-    return inter ? D / 8 : D / 8 - rot / 16;
-  }
-  __device__ void run(const uint16_t* src, uint16_t* dst, int i) const {
+// A lane's 8 channels of every head of a token: four pairs of the rotated
+// channels, or 8 plain ones behind them (rot a multiple of 8). D / 8 lanes
+// share a head row; the pairs' angles stay in registers from head to head.
+struct LaneTurn {
+  float4 c, n;
+  int lo, hi;           // its two runs of four channels
+  bool turned, inter;
+  __device__ LaneTurn(const float* cs, int rot, int interleaved, int i) : inter(interleaved != 0) {
     const int half = rot >> 1;
-    if (rot & 15) {
-      if (i >= half) {
-        dst[i + half] = src[i + half];
-        return;
+    turned = 8 * i < rot;
+    lo = turned && !inter ? 4 * i : 8 * i;
+    hi = turned && !inter ? half + 4 * i : 8 * i + 4;
+    if (turned) {
+      c = __ldg(reinterpret_cast<const float4*>(cs + 4 * i));
+      n = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * i));
+    }
+  }
+  // reads all it writes before it writes: dst may be src
+  __device__ void run(const uint16_t* src, uint16_t* dst) const {
+    uint2 a = *reinterpret_cast<const uint2*>(src + lo), b = *reinterpret_cast<const uint2*>(src + hi);
+    if (turned) {
+      if (inter) {                               // neighbours apart, and back below
+        const uint2 t = a;
+        a = make_uint2(__byte_perm(t.x, t.y, 0x5410), __byte_perm(b.x, b.y, 0x5410));
+        b = make_uint2(__byte_perm(t.x, t.y, 0x7632), __byte_perm(b.x, b.y, 0x7632));
       }
-      const int ca = inter ? 2 * i : i, cb = inter ? 2 * i + 1 : i + half;
-      float x, y;
-      turn(bf(src[ca]), bf(src[cb]), __ldg(cs + i), __ldg(cs + half + i), x, y);
-      dst[ca] = bf_rn(x);
-      dst[cb] = bf_rn(y);
-      return;
-    }
-    const uint4* s4 = reinterpret_cast<const uint4*>(src);
-    uint4* d4 = reinterpret_cast<uint4*>(dst);
-    if (inter) {
-      const uint4 v = s4[i];
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      if (8 * i < rot) {
-        const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + 4 * i));
-        const float4 n4 = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * i));
-        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, n[4] = {n4.x, n4.y, n4.z, n4.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float x, y;
-          turn(bf(w[k] & 0xffffu), bf(w[k] >> 16), c[k], n[k], x, y);
-          w[k] = pack2(x, y);
-        }
+      turn2(a.x, b.x, make_float2(c.x, c.y), make_float2(n.x, n.y));
+      turn2(a.y, b.y, make_float2(c.z, c.w), make_float2(n.z, n.w));
+      if (inter) {
+        const uint2 t = a;
+        a = make_uint2(__byte_perm(t.x, b.x, 0x5410), __byte_perm(t.x, b.x, 0x7632));
+        b = make_uint2(__byte_perm(t.y, b.y, 0x5410), __byte_perm(t.y, b.y, 0x7632));
       }
-      d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      return;
     }
-    if (i >= rot / 16) {
-      d4[i + rot / 16] = s4[i + rot / 16];
-      return;
-    }
-    const uint4 va = s4[i], vb = s4[i + rot / 16];
-    const uint32_t a[4] = {va.x, va.y, va.z, va.w}, b[4] = {vb.x, vb.y, vb.z, vb.w};
-    float c[8], n[8];
-    load8(cs + 8 * i, c);
-    load8(cs + half + 8 * i, n);
-    uint32_t oa[4], ob[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float x0, y0, x1, y1;
-      turn(bf(a[k] & 0xffffu), bf(b[k] & 0xffffu), c[2 * k], n[2 * k], x0, y0);
-      turn(bf(a[k] >> 16), bf(b[k] >> 16), c[2 * k + 1], n[2 * k + 1], x1, y1);
-      oa[k] = pack2(x0, x1);
-      ob[k] = pack2(y0, y1);
-    }
-    d4[i] = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-    d4[i + rot / 16] = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+    *reinterpret_cast<uint2*>(dst + lo) = a;
+    *reinterpret_cast<uint2*>(dst + hi) = b;
   }
 };
 
 template <int D, int GS>
-__global__ void __launch_bounds__(kThreads) rotate_rows(RotateParams p) {
-  constexpr int NS = D / kGroup, SPG = GS / kGroup, NG = D / GS;
+__global__ void __launch_bounds__(kThreads, 8) rotate_rows(RotateParams p) {
+  constexpr int NG = D / GS;
   __shared__ int before_s[kThreads / 32];
   // the key kernel may be scheduled; it waits for this grid before it reads
   asm volatile("griddepcontrol.launch_dependents;");
@@ -177,32 +154,49 @@ __global__ void __launch_bounds__(kThreads) rotate_rows(RotateParams p) {
       for (int i = tid; i < a.H_q * D; i += kThreads) a.Q_out[tok * a.H_q * D + i] = 0x7fc0u;
     return;
   }
-  const RowTurn<D> rt{a.cos_sin + size_t(pos) * a.rot, a.rot, a.interleaved};
-  const int per = rt.tasks();
-  const int nk = lead < 0 ? 0 : p.H * per, nq = a.Q ? a.H_q * per : 0;
-  for (int i = tid; i < nk + nq; i += kThreads) {
-    const bool key = i < nk;
-    const int j = key ? i : i - nk, head = j / per, task = j - head * per;
-    if (key) {
-      rt.run(a.K + (tok * p.H + head) * D, p.Kr + (size_t(row) * p.H + head) * D, task);
-    } else {
-      const size_t q = (tok * a.H_q + head) * D;
-      rt.run(a.Q + q, a.Q_out + q, task);
+  const float* cs = a.cos_sin + size_t(pos) * a.rot;
+  const int nk = lead < 0 ? 0 : p.H, heads = nk + (a.Q ? a.H_q : 0);
+  constexpr int NL = D / 8, ROWS = kThreads / NL;   // lanes of a head row, rows at a time
+  const int part = tid % NL, h0 = tid / NL;
+  auto from = [&](int h) { return h < nk ? a.K + (tok * p.H + h) * D : a.Q + (tok * a.H_q + (h - nk)) * D; };
+  auto to = [&](int h) { return h < nk ? p.Kr + (size_t(row) * p.H + h) * D : a.Q_out + (tok * a.H_q + (h - nk)) * D; };
+  if (a.rot % 8 == 0) {
+    const LaneTurn lt(cs, a.rot, a.interleaved, part);
+    for (int h = h0; h < heads; h += ROWS) lt.run(from(h), to(h));
+  } else {
+    // any even rot: a pair or a plain channel at a time
+    const int half = a.rot >> 1;
+#pragma unroll 1
+    for (int h = h0; h < heads; h += ROWS) {
+      const uint16_t* src = from(h);
+      uint16_t* dst = to(h);
+#pragma unroll 1
+      for (int j = part; j < D - half; j += NL) {
+        if (j >= half) {
+          dst[j + half] = src[j + half];
+          continue;
+        }
+        const int ca = a.interleaved ? 2 * j : j, cb = a.interleaved ? 2 * j + 1 : j + half;
+        float x, y;
+        turn(bf(src[ca]), bf(src[cb]), __ldg(cs + j), __ldg(cs + half + j), x, y);
+        dst[ca] = bf_rn(x);
+        dst[cb] = bf_rn(y);
+      }
     }
   }
   if (lead < 0) return;
-  // ---- values: one thread per 32-channel sub-group (a group's sub-groups in
-  // consecutive lanes; every lane takes part in the shuffles)
-  for (int i0 = warp * 32; i0 < p.H * NS; i0 += kThreads) {
-    const int i = i0 + lane;
-    const bool live = i < p.H * NS;
-    const int head = live ? i / NS : 0, sg = i % NS;
-    uint32_t w0, w1;
-    const GroupParams gp = code_values<GS>(a.V + (tok * p.H + head) * D + sg * kGroup, w0, w1);
+  // ---- values: 8 channels a lane (every lane takes part in the shuffles)
+  for (int w0 = warp * (32 / NL); w0 < p.H; w0 += ROWS) {
+    const int h = w0 + lane / NL;
+    const bool live = h < p.H;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (live) v = *(reinterpret_cast<const uint4*>(a.V + (tok * p.H + h) * D) + part);
+    uint32_t bits;
+    const GroupParams gp = code_values8<GS>(v, bits);
     if (live) {
-      const size_t at = (size_t(lead) * p.H + head) * size_t(p.table ? p.page : p.cap) + off;
-      *reinterpret_cast<uint2*>(p.v_code + at * (D / 16) + sg * 2) = make_uint2(w0, w1);
-      if (sg % SPG == 0) p.v_sz[at * NG + sg / SPG] = uint32_t(gp.s_bits) | (uint32_t(gp.z_bits) << 16);
+      const size_t at = (size_t(lead) * p.H + h) * size_t(p.table ? p.page : p.cap) + off;
+      reinterpret_cast<uint16_t*>(p.v_code)[at * NL + part] = uint16_t(bits);
+      if (part % (GS / 8) == 0) p.v_sz[at * NG + part / (GS / 8)] = uint32_t(gp.s_bits) | (uint32_t(gp.z_bits) << 16);
     }
   }
 }
