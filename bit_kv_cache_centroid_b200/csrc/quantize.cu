@@ -1179,6 +1179,19 @@ cudaError_t launch_d(const QuantizeArgs& a, cudaStream_t s) {
     if (mp <= 8) return launch_cfg<D, 8, 1, GS>(a, s);
     return launch_cfg<D, 16, 1, GS>(a, s);
   }
+  // Middling appends whose tiles of 128 keys would leave half the SMs without
+  // one: 4 keys per warp, tiles of 32 (d = 128, 64 centres, 8 heads, rotation
+  // and queries' pass included: 512 keys 58 -> 32 us, 1,152 keys 60 -> 34;
+  // with tiles for more SMs than that the wide tiles read the table less often)
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (2LL * ((a.B * a.n_new + 127) / 128) * a.H <= sms) {
+    if (mp <= 1) return launch_cfg<D, 1, 4, GS>(a, s);
+    if (mp <= 2) return launch_cfg<D, 2, 4, GS>(a, s);
+    if (mp <= 4) return launch_cfg<D, 4, 4, GS>(a, s);
+    if (mp <= 8) return launch_cfg<D, 8, 4, GS>(a, s);
+  }
   if (mp <= 1) return launch_cfg<D, 1, 16, GS>(a, s);
   if (mp <= 2) return launch_cfg<D, 2, 16, GS>(a, s);
   if (mp <= 4) return launch_cfg<D, 4, 16, GS>(a, s);
