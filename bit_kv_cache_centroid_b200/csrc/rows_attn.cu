@@ -1062,81 +1062,154 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
 // merges
 // ---------------------------------------------------------------------------
 
-// One warp: log-sum-exp of one row's pieces, those of CTAs c0 (slot 1) and
-// c0 + 1 .. c1 (slot 0); lane i holds channels i, i + 32, ...
-template <int D>
-__device__ __forceinline__ void merge_pieces(const float* part_o, const float2* part_ml, int N, int row, int c0, int c1,
-                                            long long T, int C, int lane, float& m, float& l, float (&o)[D / 32]) {
-  m = -INFINITY;
-  for (int s0 = c0; s0 <= c1; s0 += 32) {
-    const int c = s0 + lane;
-    if (c <= c1 && part_begin(T, c, C) < part_begin(T, c + 1, C)) {
-      const float2 ml = part_ml[(size_t(c) * 2 + (c == c0)) * N + row];
-      if (!(ml.y == 0.0f)) m = fmaxf(m, ml.x);
+// A lane's W = D / 32 channels of a row: W * lane ...
+template <int W>
+struct RowPart {
+  float v[W];
+  __device__ __forceinline__ static RowPart load(const float* row, int lane) {
+    RowPart r;
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {              // (the split decode kernel's rows start on 8 bytes)
+      const float2 x = *reinterpret_cast<const float2*>(row + W * lane + i);
+      r.v[i] = x.x; r.v[i + 1] = x.y;
     }
+    return r;
+  }
+  // += f * o, o not looked at where f is 0 (an empty or absent piece)
+  __device__ __forceinline__ void add(float f, const RowPart& o) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = f == 0.0f ? v[i] : fmaf(f, o.v[i], v[i]);
+  }
+  // the row of the output, divided by its sum l (0: an empty row)
+  __device__ __forceinline__ void store(void* out, int out_dtype, size_t row, int lane, float l) const {
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    float* f = static_cast<float*>(out) + row * (W * 32) + W * lane;
+    __nv_bfloat16* b = static_cast<__nv_bfloat16*>(out) + row * (W * 32) + W * lane;
+    if (out_dtype == KV2_OUT_F32) {
+      if constexpr (W == 4) *reinterpret_cast<float4*>(f) = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+      else *reinterpret_cast<float2*>(f) = make_float2(v[0] * inv, v[1] * inv);
+    } else {
+      if constexpr (W == 4) *reinterpret_cast<uint2*>(b) = make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+      else *reinterpret_cast<uint32_t*>(b) = pack_bf16(v[0] * inv, v[1] * inv);
+    }
+  }
+};
+
+// One warp: log-sum-exp of n partial results of a row; ml(i) is the maximum
+// and the sum of part i (sum 0: an empty part), o(i) its row of channels.
+template <int W, class ML, class O>
+__device__ __forceinline__ void merge_parts(int n, int lane, ML ml, O o, float& m, float& l, RowPart<W>& acc) {
+  m = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const float2 x = ml(i);
+    if (!(x.y == 0.0f)) m = fmaxf(m, x.x);
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   l = 0.0f;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
-  for (int s0 = c0; s0 <= c1; s0 += 32) {
-    const int c = s0 + lane;
+  for (int i = 0; i < W; ++i) acc.v[i] = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
     float f = 0.0f;
-    if (c <= c1 && part_begin(T, c, C) < part_begin(T, c + 1, C)) {
-      const float2 ml = part_ml[(size_t(c) * 2 + (c == c0)) * N + row];
-      if (!(ml.y == 0.0f)) {
-        f = exp2f(ml.x - m);
-        l = fmaf(f, ml.y, l);
+    if (i0 + lane < n) {
+      const float2 x = ml(i0 + lane);
+      if (!(x.y == 0.0f)) {
+        f = exp2f(x.x - m);
+        l = fmaf(f, x.y, l);
       }
     }
-    const int n = min(32, c1 - s0 + 1);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float fk = __shfl_sync(0xffffffffu, f, k);
-      if (fk == 0.0f) continue;                   // an empty or absent piece (uniform over the warp)
-      const float* po = part_o + ((size_t(s0 + k) * 2 + (s0 + k == c0)) * N + row) * D;
+    // eight rows in flight together
+    const int end = min(32, n - i0);
+    for (int k = 0; k < end; k += 8) {
+      RowPart<W> x[8];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(fk, po[i * 32 + lane], o[i]);
+      for (int u = 0; u < 8; ++u)
+        if (k + u < end) x[u] = RowPart<W>::load(o(i0 + k + u), lane);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float fk = __shfl_sync(0xffffffffu, f, (k + u) & 31);
+        if (k + u < end) acc.add(fk, x[u]);
+      }
     }
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
 }
-
+// the pieces of CTAs c0 (slot 1) and c0 + 1 .. c1 (slot 0); T >= C or a part may be empty
 template <int D>
-__device__ __forceinline__ void store_row(void* out, int out_dtype, size_t row, int lane, float l, const float (&o)[D / 32]) {
-  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const size_t at = row * D + i * 32 + lane;
-    if (out_dtype == KV2_OUT_F32) static_cast<float*>(out)[at] = o[i] * inv;
-    else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(o[i] * inv);
-  }
+__device__ __forceinline__ void merge_pieces(const RowsParams& p, int N, int row, int c0, int c1, long long T, int C,
+                                            int lane, float& m, float& l, RowPart<D / 32>& o) {
+  auto at = [&](int i) { return (size_t(c0 + i) * 2 + (i == 0)) * N + row; };
+  merge_parts<D / 32>(
+      c1 - c0 + 1, lane,
+      [&](int i) { return T >= C || part_begin(T, c0 + i, C) < part_begin(T, c0 + i + 1, C) ? p.part_ml[at(i)] : make_float2(0.0f, 0.0f); },
+      [&](int i) { return p.part_o + at(i) * D; }, m, l, o);
 }
 
-// One source: block (c - 1, .) merges the unit that the border before CTA c
-// cuts, if it is the unit's first border; one warp per row.
+// One source: blocks (c - 1, .) merge the unit that the border before CTA c
+// cuts, kCutRows rows a block; the blocks of a unit's K borders share its rows
+// (with parts that are empty, T < C, the first border has them all). The way
+// to the rows (list, lengths, borders) is a chain of reads, so a warp takes
+// several rows, and where a unit has just two pieces, as most do with many
+// query rows, all their reads go out together. Cross attention of 4 x 509
+// queries over 2,047 keys and 32 heads: 11 us for 26.7 us with one row a warp.
+constexpr int kCutRows = 64;
 template <int D, int N>
 __global__ void __launch_bounds__(256) rows_merge_cut(const __grid_constant__ RowsParams p, int C) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int W = D / 32, R = kCutRows / 8;
   const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 at = p.cta[c];
   const long long T = *p.total, lo = part_begin(T, c, C);
   if (lo >= part_begin(T, c + 1, C)) return;
-  const int4 at = p.cta[c];
   if (at.w == 0) return;                          // no unit is cut here
   const int G = p.H_q / p.H_kv;
   const int ql = seq_queries(p.src[0], at.y), RB = blocks_of<N>(ql, G);
   const long long u = lo - at.w;                  // position of the unit's first tile
   const int c0 = part_of(u, T, C), c1 = part_of(u + tiles_of(seq_len(p.src[0], at.y)) - 1, T, C);
-  if (part_begin(T, c0 + 1, C) != lo) return;     // an earlier border of the same unit
-  const int row = blockIdx.y * 8 + warp;
-  const int ri = (at.z % RB) * N + row;
-  if (ri >= ql * G) return;
-  float m, l, o[D / 32];
-  merge_pieces<D>(p.part_o, p.part_ml, N, row, c0, c1, T, C, lane, m, l, o);
-  const size_t gr = (size_t(at.y) * p.src[0].Nq + ri / G) * p.H_q + (at.z / RB) * G + ri % G;
-  store_row<D>(p.out, p.out_dtype, gr, lane, l, o);
+  const int K = T < C ? 1 : c1 - c0, k = T < C ? 0 : c - 1 - c0;
+  if (T < C && part_begin(T, c0 + 1, C) != lo) return;
+  const int first = blockIdx.y * kCutRows + warp * R, base = (at.z % RB) * N, h = at.z / RB;
+  auto out_row = [&](int row) {
+    const int ri = base + row, i = p.per_head(ri);
+    return (size_t(at.y) * p.src[0].Nq + i) * p.H_q + h * G + (ri - i * G);
+  };
+  const int rows = min(R, ql * G - base - first);
+  if (c1 == c0 + 1) {
+    const size_t a0 = (size_t(c0) * 2 + 1) * N + first, a1 = size_t(c1) * 2 * N + first;
+#pragma unroll
+    for (int i0 = 0; i0 < R; i0 += 4) {
+      RowPart<W> x[4], y[4];
+      float2 mx[4], my[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i >= rows) break;
+        mx[i] = p.part_ml[a0 + i0 + i];
+        my[i] = p.part_ml[a1 + i0 + i];
+        x[i] = RowPart<W>::load(p.part_o + (a0 + i0 + i) * D, lane);
+        y[i] = RowPart<W>::load(p.part_o + (a1 + i0 + i) * D, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i >= rows) break;
+        const bool ex = mx[i].y == 0.0f, ey = my[i].y == 0.0f;
+        const float m = fmaxf(ex ? -INFINITY : mx[i].x, ey ? -INFINITY : my[i].x);
+        const float fx = ex ? 0.0f : exp2f(mx[i].x - m), fy = ey ? 0.0f : exp2f(my[i].x - m);
+        RowPart<W> o{};
+        o.add(fx, x[i]);
+        o.add(fy, y[i]);
+        o.store(p.out, p.out_dtype, out_row(first + i0 + i), lane, fmaf(fx, mx[i].y, fy * my[i].y));
+      }
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int i = (k + K - first % K) % K; i < rows; i += K) {   // the unit's rows k, k + K, ...
+    float m, l;
+    RowPart<W> o;
+    merge_pieces<D>(p, N, first + i, c0, c1, T, C, lane, m, l, o);
+    o.store(p.out, p.out_dtype, out_row(first + i), lane, l);
+  }
 }
 
 // Shared prefix: one warp per (sequence, query head) joins the row's result
@@ -1149,40 +1222,15 @@ __global__ void __launch_bounds__(256) rows_merge_shared(const __grid_constant__
   if (gr >= p.dir_rows) return;
   const int G = p.H_q / p.H_kv, hq = int(gr % p.H_q), h = hq / G, g = hq % G;
   const long long T = *p.total;
-  float m[2], l[2], o[2][D / 32];
+  float m[2], l[2];
+  RowPart<D / 32> o[2];
   if (p.split_part) {
-    // own cache: lane s of the warp weighs split s (32 at a time)
+    // own cache: the splits' rows [G][D + 2], maximum and sum behind the channels
     const float* base = p.split_part + (gr / p.H_q * p.H_kv + h) * size_t(p.splits) * G * (D + 2) + size_t(g) * (D + 2);
     const size_t step = size_t(G) * (D + 2);
-    float top = -INFINITY;
-    for (int s0 = lane; s0 < p.splits; s0 += 32)
-      if (base[s0 * step + D + 1] != 0.0f) top = fmaxf(top, base[s0 * step + D]);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    m[1] = top;
-    l[1] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[1][k] = 0.0f;
-    for (int s0 = 0; s0 < p.splits; s0 += 32) {
-      float f = 0.0f;
-      if (s0 + lane < p.splits) {
-        const float ls = base[(s0 + lane) * step + D + 1];
-        if (ls != 0.0f) {
-          f = exp2f(base[(s0 + lane) * step + D] - top);
-          l[1] = fmaf(f, ls, l[1]);
-        }
-      }
-      const int n = min(32, p.splits - s0);
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const float fj = __shfl_sync(0xffffffffu, f, j);
-        if (fj == 0.0f) continue;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) o[1][k] = fmaf(fj, base[(s0 + j) * step + k * 32 + lane], o[1][k]);
-      }
-    }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
+    merge_parts<D / 32>(
+        p.splits, lane, [&](int i) { return *reinterpret_cast<const float2*>(base + i * step + D); },
+        [&](int i) { return base + i * step; }, m[1], l[1], o[1]);
   }
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -1198,18 +1246,17 @@ __global__ void __launch_bounds__(256) rows_merge_shared(const __grid_constant__
       const float2 ml = p.dir_ml[size_t(s) * p.dir_rows + gr];
       m[s] = ml.x;
       l[s] = ml.y;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) o[s][k] = p.dir_o[(size_t(s) * p.dir_rows + gr) * D + k * 32 + lane];
+      o[s] = RowPart<D / 32>::load(p.dir_o + (size_t(s) * p.dir_rows + gr) * D, lane);
     } else {
-      merge_pieces<D>(p.part_o, p.part_ml, N, ri % N, c0, c1, T, C, lane, m[s], l[s], o[s]);
+      merge_pieces<D>(p, N, ri % N, c0, c1, T, C, lane, m[s], l[s], o[s]);
     }
   }
   const float mm = fmaxf(l[0] == 0.0f ? -INFINITY : m[0], l[1] == 0.0f ? -INFINITY : m[1]);
   const float f0 = l[0] == 0.0f ? 0.0f : exp2f(m[0] - mm), f1 = l[1] == 0.0f ? 0.0f : exp2f(m[1] - mm);
-  float r[D / 32];
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) r[k] = (f0 == 0.0f ? 0.0f : f0 * o[0][k]) + (f1 == 0.0f ? 0.0f : f1 * o[1][k]);
-  store_row<D>(p.out, p.out_dtype, size_t(gr), lane, f0 * l[0] + f1 * l[1], r);
+  RowPart<D / 32> r{};
+  r.add(f0, o[0]);
+  r.add(f1, o[1]);
+  r.store(p.out, p.out_dtype, size_t(gr), lane, f0 * l[0] + f1 * l[1]);
 }
 
 // ---------------------------------------------------------------------------
@@ -1300,7 +1347,7 @@ cudaError_t launch_cfg(const RowsParams& p, const RowsPlan& pl, cudaStream_t s) 
   e = cudaLaunchKernelEx(&cfg, kern, q);
   if (e != cudaSuccess || (!both && pl.C == 1)) return e;
   cfg = cudaLaunchConfig_t{};
-  cfg.gridDim = both ? dim3(unsigned((pl.rows + 7) / 8)) : dim3(pl.C - 1, Cfg::N / 8);
+  cfg.gridDim = both ? dim3(unsigned((pl.rows + 7) / 8)) : dim3(pl.C - 1, Cfg::N / kCutRows);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = attr;
