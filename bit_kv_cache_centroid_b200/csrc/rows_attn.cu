@@ -143,11 +143,11 @@ struct RCfg {
   static constexpr uint32_t OFF_RAW = OFF_A + KS * A_BYTES;
   static constexpr uint32_t OFF_U = OFF_RAW + RS * RAW_BYTES;
   static constexpr uint32_t OFF_FRAG = OFF_U + X * U_BYTES;             // P fragments [D/16][2][2][32] uint2
-  static constexpr uint32_t OFF_UF = OFF_FRAG + D / 16 * 2 * 2 * 32 * 8;    // fp32 products of more row blocks than warps
-  static constexpr uint32_t OFF_SCR = OFF_UF + (N > PW * 16 ? N * 64 : 0);  // row scales, ring of 4 units
-  static constexpr uint32_t OFF_QE = OFF_SCR + 4 * N * 4;               // row exponents of the unit being loaded
-  static constexpr uint32_t OFF_ML = OFF_QE + N * 4;                    // maxima and sums of both groups, float2 [2][kRows]
-  static constexpr uint32_t OFF_BAR = OFF_ML + 2 * kRows * 8;
+  static constexpr uint32_t OFF_SCR = OFF_FRAG + D / 16 * 2 * 2 * 32 * 8;   // row scales, ring of 4 units
+  static constexpr uint32_t OFF_ML = OFF_SCR + 4 * N * 4;                    // maxima and sums of both groups, float2 [2][kRows]
+  // output rows on their way out of WIDE units, 2 KB a softmax warp
+  static constexpr uint32_t OFF_STG = OFF_ML + 2 * kRows * 8;
+  static constexpr uint32_t OFF_BAR = OFF_STG + (WIDE ? SW * 2048 : 0);
   static constexpr uint32_t SMEM = OFF_BAR + 288 + 1024;
   static constexpr uint32_t kTmemCols = 512;           // S of both groups, O of both groups
   // Q, U, Khat, A K-major; Vhat by channels
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
       mbar_init(bar + B_RFULL + 8 * i, 1);
       mbar_init(bar + B_REMPTY + 8 * i, 2 * PW);
     }
-    mbar_init(bar + B_QFULL, PW);
+    mbar_init(bar + B_QFULL, N / 16);
     mbar_init(bar + B_QEMPTY, 1);
     mbar_init(bar + B_FINAL, 1);
     mbar_init(bar + B_NEVER, 1);
@@ -575,6 +575,9 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
     const int pt = tid - (values ? Cfg::kValueWarp : SW) * 32, pw = pt >> 5;
     const int row = pw * 16 + (lane & 7) + 8 * (lane >> 4), part = (lane >> 3) & 1;
     uint2* frag = reinterpret_cast<uint2*>(smem + Cfg::OFF_FRAG);
+    constexpr int QW = N / 16;                    // warps that load query rows
+    const int qw = values ? pw : PW + pw;
+    static_assert(QW <= 2 * PW, "a warp per 16 query rows");
     int t = 0, seg = 0, frag_src = -1, frag_h = -1;
     // the warp's operand writes are done: one arrival for all lanes
     auto arrive_warp = [&](uint32_t b) __attribute__((always_inline)) {
@@ -583,53 +586,60 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
       if (lane == 0) mbar_arrive(b);
     };
 
-    // The query rows of a unit, by the value warps: copied raw, 16 bytes per
-    // thread and step; their product with the basis (bf16 query, exact; P as two
-    // bf16 numbers, 2^-16), 16 rows per warp; then both scaled by 2^e per row,
-    // max(|q|, |u|) 2^e < 2^15, to fp16.
+    // The query rows of a unit, a block of 16 rows a warp (of WIDE units by all
+    // producers, else by the value warps), which waits for no other: copied raw,
+    // 16 bytes a lane and step; their product with the basis (bf16 query, exact; P as two bf16
+    // numbers, 2^-16); then both scaled by 2^e per row, max(|q|, |u|) 2^e < 2^15,
+    // to fp16.
     auto load_queries = [&]() __attribute__((always_inline)) {
       const RowsSource& s = p.src[w.src];
-      constexpr int LPR = D / 8, STEP = PW * 32 / LPR;      // lanes per row, rows per step
-      const int c = pt % LPR, r0 = pt / LPR;
+      constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = 16 / RPS;      // lanes per row, rows per step, steps per block
+      const int c = lane % LPR, r0 = lane / LPR;
       uint8_t* qt = smem + Cfg::OFF_Q;
       float* scr = reinterpret_cast<float*>(smem + Cfg::OFF_SCR) + (seg & 3) * N;
-      int* qe = reinterpret_cast<int*>(smem + Cfg::OFF_QE);
       auto q_off = [&](int rx, int k) { return (rx / kRows) * Cfg::Q_BYTES + int(sw128_off(rx % kRows, k)); };
       // (rows that do not exist are not loaded: their scores are not looked at)
       const int rows = min(N, (w.ql * G - w.rb * N + 15) & ~15);
+      const int rb = qw * 16;
       if (seg > 0) mbar_wait_or_abort(bar + B_QEMPTY, (seg - 1) & 1, p.budget, abort);
-#pragma unroll 1
-      for (int rx = r0; rx < rows; rx += STEP) {
-        const int ri = w.rb * N + rx, i = p.per_head(ri);
-        const bool in = ri < w.ql * G;
-        const size_t gr = in ? (size_t(w.b) * s.Nq + i) * p.H_q + w.h * G + (ri - i * G) : 0;
-        copy16(sb + Cfg::OFF_Q + q_off(rx, c), p.Q + gr * D + c * 8, in);
-      }
-      float acc[2][4];
-      if (s.r > 0) {
-        if (w.src != frag_src || w.h != frag_h) {
-          const float* Ph = s.P + size_t(w.h) * D * s.r;
-#pragma unroll 1
-          for (int i = pt; i < D / 16 * 2 * 32; i += PW * 32) {
-            const int l = i & 31, nt = (i >> 5) & 1, ks = i >> 6;
-            const int n = nt * 8 + (l >> 2), k = ks * 16 + 2 * (l & 3);
-            float hi[4], lo[4];
+      if (rb < rows) {
+        // lane i finds row i, and the lanes that copy it get its place from there (~0: no such row)
+        const int ri = w.rb * N + rb + (lane & 15), i = p.per_head(ri);
+        const unsigned long long gr =
+            ri < w.ql * G ? ((static_cast<unsigned long long>(w.b) * s.Nq + i) * p.H_q + w.h * G + (ri - i * G)) * D : ~0ull;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float y = n < s.r ? __ldg(Ph + size_t(k + (e & 1) + 8 * (e >> 1)) * s.r + n) : 0.0f;
-              hi[e] = __bfloat162float(__float2bfloat16_rn(y));
-              lo[e] = y - hi[e];
-            }
-            frag[((ks * 2 + nt) * 2 + 0) * 32 + l] = make_uint2(pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3]));
-            frag[((ks * 2 + nt) * 2 + 1) * 32 + l] = make_uint2(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]));
-          }
-          frag_src = w.src;
-          frag_h = w.h;
+        for (int st = 0; st < STEPS; ++st) {
+          const unsigned long long at = __shfl_sync(0xffffffffu, gr, st * RPS + r0);
+          const bool in = at != ~0ull;
+          copy16(sb + Cfg::OFF_Q + q_off(rb + st * RPS + r0, c), p.Q + (in ? at : 0) + c * 8, in);
         }
-        copy_wait();
-        bar_sync(1, PW * 32);                     // rows and fragments are there
+      }
+      if (s.r > 0 && (w.src != frag_src || w.h != frag_h)) {
+        bar_sync(1, QW * 32);                     // the fragments before are read
+        const float* Ph = s.P + size_t(w.h) * D * s.r;
 #pragma unroll 1
-        for (int rb = pw * 16; rb < rows; rb += PW * 16) {
+        for (int i = qw * 32 + lane; i < D / 16 * 2 * 32; i += QW * 32) {
+          const int l = i & 31, nt = (i >> 5) & 1, ks = i >> 6;
+          const int n = nt * 8 + (l >> 2), k = ks * 16 + 2 * (l & 3);
+          float hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = n < s.r ? __ldg(Ph + size_t(k + (e & 1) + 8 * (e >> 1)) * s.r + n) : 0.0f;
+            hi[e] = __bfloat162float(__float2bfloat16_rn(y));
+            lo[e] = y - hi[e];
+          }
+          frag[((ks * 2 + nt) * 2 + 0) * 32 + l] = make_uint2(pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3]));
+          frag[((ks * 2 + nt) * 2 + 1) * 32 + l] = make_uint2(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]));
+        }
+        frag_src = w.src;
+        frag_h = w.h;
+        bar_sync(1, QW * 32);                     // the fragments are there
+      }
+      copy_wait();
+      __syncwarp();
+      if (rb < rows) {
+        float acc[2][4], um = 0.0f;               // um: largest |u| of row lane % 16
+        if (s.r > 0) {
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -646,7 +656,7 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
                 mma16816(acc[nt], a, bb.x, bb.y);
               }
           }
-          // largest |u| of rows lane / 4 and lane / 4 + 8, for the threads that scale them
+          // rows lane / 4 and lane / 4 + 8
           float u0 = fmaxf(fmaxf(fabsf(acc[0][0]), fabsf(acc[0][1])), fmaxf(fabsf(acc[1][0]), fabsf(acc[1][1])));
           float u1 = fmaxf(fmaxf(fabsf(acc[0][2]), fabsf(acc[0][3])), fmaxf(fabsf(acc[1][2]), fabsf(acc[1][3])));
 #pragma unroll
@@ -654,67 +664,43 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
             u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
             u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
           }
-          if ((lane & 3) == 0) {
-            scr[rb + (lane >> 2)] = u0;
-            scr[rb + (lane >> 2) + 8] = u1;
-          }
-          if constexpr (N > PW * 16) {
-            // more blocks than warps: kept in shared memory until they are scaled
-            float* uf = reinterpret_cast<float*>(smem + Cfg::OFF_UF) + rb * 16;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const int n = nt * 8 + 2 * (lane & 3);
-              *reinterpret_cast<float2*>(uf + (lane >> 2) * 16 + n) = make_float2(acc[nt][0], acc[nt][1]);
-              *reinterpret_cast<float2*>(uf + ((lane >> 2) + 8) * 16 + n) = make_float2(acc[nt][2], acc[nt][3]);
-            }
-          }
+          u0 = __shfl_sync(0xffffffffu, u0, (lane & 7) * 4);
+          u1 = __shfl_sync(0xffffffffu, u1, (lane & 7) * 4);
+          um = lane & 8 ? u1 : u0;
         }
-        bar_sync(1, PW * 32);                     // the raw rows are read
-      } else {
-        copy_wait();
-      }
-#pragma unroll 1
-      for (int rx = r0; rx < rows; rx += STEP) {
-        uint4* at = reinterpret_cast<uint4*>(qt + q_off(rx, c));
-        const uint4 v = *at;
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        uint32_t am = 0;
+        // lanes i and i + 16 scale a half of row i each (no lane needs another's
+        // row, and eight lanes' chunks fall on eight bank groups)
+        const int mine = rb + (lane & 15), k0 = (lane >> 4) * (D / 16);
+        __nv_bfloat162 am = __float2bfloat162_rn(0.0f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) am = __vmaxu2(am, u[i] & 0x7fff7fffu);
-        am = max(am & 0xffffu, am >> 16);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4*>(qt + q_off(mine, k0 + k));
+          const uint32_t u[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-        const float top = fmaxf(__uint_as_float(am << 16), s.r > 0 ? scr[rx] : 0.0f);
-        const int e = top > 0.0f && top < INFINITY && am < 0x7f80u ? min(max(15 - exp_above(top), -126), 64) : 0;
+          for (int i = 0; i < 4; ++i) am = __hmax2(am, *reinterpret_cast<const __nv_bfloat162*>(&u[i]));
+        }
+        // (a NaN beside finite values is left out here, and reaches the row's scores through q)
+        float top = fmaxf(__low2float(am), __high2float(am));
+        top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), um);
+        const int e = top > 0.0f && top < INFINITY ? min(max(15 - exp_above(top), -126), 64) : 0;
         const float qmul = p.q_sign * pow2(e);
-        uint32_t o4[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o4[i] = pack_f16(__uint_as_float(u[i] << 16) * qmul, __uint_as_float(u[i] & 0xffff0000u) * qmul);
-        *at = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-        __syncwarp();                             // scr[rx] is read by the row's lanes
-        if (c == 0) {
-          qe[rx] = e;
-          scr[rx] = p.scale_log2 * pow2(-e);
+        for (int k = 0; k < D / 16; ++k) {
+          uint4* at = reinterpret_cast<uint4*>(qt + q_off(mine, k0 + k));
+          const uint4 v = *at;
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o4[i] = pack_f16(__uint_as_float(u[i] << 16) * qmul, __uint_as_float(u[i] & 0xffff0000u) * qmul);
+          *at = make_uint4(o4[0], o4[1], o4[2], o4[3]);
         }
-      }
-      if (s.r > 0) {
-        bar_sync(1, PW * 32);                     // the rows' exponents are there
-#pragma unroll 1
-        for (int rb = pw * 16; rb < rows; rb += PW * 16) {
+        if (lane < 16) scr[mine] = p.scale_log2 * pow2(-e);
+        const int ea = __shfl_sync(0xffffffffu, e, lane >> 2), eb = __shfl_sync(0xffffffffu, e, (lane >> 2) + 8);
+        if (s.r > 0) {
           uint8_t* ut = smem + Cfg::OFF_U + (rb / kRows) * Cfg::U_BYTES;
-          const int ra = rb + (lane >> 2), rt = ra % kRows, q = (lane & 3) * 4;
-          if constexpr (N > PW * 16) {
-            const float* uf = reinterpret_cast<const float*>(smem + Cfg::OFF_UF) + rb * 16;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const int n = nt * 8 + 2 * (lane & 3);
-              const float2 x = *reinterpret_cast<const float2*>(uf + (lane >> 2) * 16 + n);
-              const float2 y = *reinterpret_cast<const float2*>(uf + ((lane >> 2) + 8) * 16 + n);
-              acc[nt][0] = x.x; acc[nt][1] = x.y; acc[nt][2] = y.x; acc[nt][3] = y.y;
-            }
-          }
-          const float ma = p.q_sign * pow2(qe[ra]), mb = p.q_sign * pow2(qe[ra + 8]);
+          const int rt = (rb + (lane >> 2)) % kRows, q = (lane & 3) * 4;
+          const float ma = p.q_sign * pow2(ea), mb = p.q_sign * pow2(eb);
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             *reinterpret_cast<uint32_t*>(ut + nosw_off(rt, nt) + q) = pack_f16(acc[nt][0] * ma, acc[nt][1] * ma);
@@ -733,8 +719,8 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
     for (; w.more(); w.next(p), ++seg) {
       const RowsSource& s = p.src[w.src];
       const int cnt = w.count(), gshift = s.gshift, szb = (D >> gshift) * 4;
+      if (qw < QW) load_queries();
       if (values) {
-        load_queries();
 #pragma unroll 1
         for (int jj = 0; jj < cnt; ++jj, ++t) {
           const bool have = (w.j + jj) * kKeys + row < w.len;
@@ -1012,6 +998,46 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
           if (dead) {
 #pragma unroll
             for (int q = 0; q < 32; ++q) v[q] = __int_as_float(0x7fc00000);
+          }
+          if constexpr (WIDE) {
+            // 64 bytes a row (16 fp32 or 32 bf16 channels) through shared memory, so that
+            // four lanes write a row's: a row a lane would take 32 lines a store, and the
+            // load/store unit that the next unit's queries pass through
+            const bool f32 = !whole || !p.out || p.out_dtype == KV2_OUT_F32;
+            const float mul = whole && p.out ? inv : 1.0f;
+            uint8_t* stg = smem + Cfg::OFF_STG + warp * 2048;
+            const unsigned long long mine =
+                !row_ok ? 0ull
+                : !whole || !p.out ? reinterpret_cast<unsigned long long>(po + c0)
+                                   : reinterpret_cast<unsigned long long>(p.out) + (gr * D + c0) * (f32 ? 4 : 2);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (half && !f32) break;
+              uint4 o4[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (f32) {
+                  const float* f = v + 16 * half + 4 * q;
+                  o4[q] = make_uint4(__float_as_uint(f[0] * mul), __float_as_uint(f[1] * mul), __float_as_uint(f[2] * mul), __float_as_uint(f[3] * mul));
+                } else {
+                  const float* f = v + 8 * q;
+                  o4[q] = make_uint4(pack_bf16(f[0] * mul, f[1] * mul), pack_bf16(f[2] * mul, f[3] * mul),
+                                     pack_bf16(f[4] * mul, f[5] * mul), pack_bf16(f[6] * mul, f[7] * mul));
+                }
+              }
+              __syncwarp();                       // the rows before are read
+#pragma unroll
+              for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stg + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16) = o4[q];
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int rr = i * 8 + (lane >> 2);
+                const unsigned long long to = __shfl_sync(0xffffffffu, mine, rr);
+                const uint4 x = *reinterpret_cast<const uint4*>(stg + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
+                if (to) *reinterpret_cast<uint4*>(to + half * 64 + (lane & 3) * 16) = x;
+              }
+            }
+            continue;
           }
           if (!row_ok) continue;
           if (!whole || !p.out) {
