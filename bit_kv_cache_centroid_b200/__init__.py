@@ -162,6 +162,14 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream, dev):
+    """Context in which what a call allocates belongs to the call's stream, so
+    that its memory is not handed out again before the call has ended."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream: on {stream.device}, expected {dev}")
+    return torch.cuda.stream(stream)
+
+
 class Cache:
     """Device buffers of one packed cache (layout of include/kv2.h) plus the
     read-only centroid table and fitted statistics it points to."""
@@ -484,7 +492,7 @@ def kv2_rotary_append(cache: Cache, rotary: Rotary, K: torch.Tensor, V: torch.Te
         _need("Q", Q, (cache.B, n_new, H_q, cache.d), _BITS16, dev)
     elif Q_out is not None:
         raise ValueError("Q_out without Q")
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _on(stream, dev):
         if Q is not None:
             Q_out = torch.zeros_like(Q) if Q_out is None else Q_out
             _need("Q_out", Q_out, Q.shape, _BITS16, dev)
@@ -537,7 +545,7 @@ def kv2_attention_cross(cache: Cache, lens, Q: torch.Tensor, sm_scale: float, ou
         if t is not None:
             _need(name, t, (B,), (torch.int32,), dev)
     max_len = cache.capacity if max_len is None else int(max_len)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _on(stream, dev):
         need = kv2_attention_cross_workspace_size(cache, H_q, Nq, max_len) if ws is None else 0
         out, ws = _rows_call(Q, Q.shape, out_dtype, out, ws, need)
         d = cache.desc()
@@ -574,7 +582,7 @@ def kv2_attention_shared(prefix: Cache, prefix_lens, cache: Cache, lens, Q: torc
             _need(name, t, (n,), (torch.int32,), dev)
     max_prefix_len = prefix.capacity if max_prefix_len is None else int(max_prefix_len)
     max_len = cache.capacity if max_len is None else int(max_len)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _on(stream, dev):
         need = kv2_attention_shared_workspace_size(prefix, cache, H_q, max_prefix_len, max_len) if ws is None else 0
         out, ws = _rows_call(Q, Q.shape, out_dtype, out, ws, need)
         p, d = prefix.desc(), cache.desc()

@@ -71,7 +71,7 @@ constexpr float kTrail = 7.0f;         // a score this far above the running max
 // A unit begins with kLead positions of the work list that hold no tile: its
 // query rows, first maxima and output rows take about as long as that many key
 // tiles, so parts with many short units get fewer tiles.
-constexpr int kLead = 4;
+constexpr int kLead = 2;
 
 struct RowsSource {
   const uint32_t* k_code;
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
         // row, and eight lanes' chunks fall on eight bank groups)
         const int mine = rb + (lane & 15), k0 = (lane >> 4) * (D / 16);
         __nv_bfloat162 am = __float2bfloat162_rn(0.0f);
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < D / 16; ++k) {
           const uint4 v = *reinterpret_cast<const uint4*>(qt + q_off(mine, k0 + k));
           const uint32_t u[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
         top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), um);
         const int e = top > 0.0f && top < INFINITY ? min(max(15 - exp_above(top), -126), 64) : 0;
         const float qmul = p.q_sign * pow2(e);
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < D / 16; ++k) {
           uint4* at = reinterpret_cast<uint4*>(qt + q_off(mine, k0 + k));
           const uint4 v = *at;

@@ -429,9 +429,12 @@ kv2_status kv2_attention_chunk(const kv2_cache* cache, int len, const uint16_t* 
 /*
  * Workspace for kv2_attention_cross, in bytes: a 256-byte header whose first
  * 32-bit word is the sticky error word, the tile list's bookkeeping (8 bytes
- * per sequence, 16 per CTA), and for each CTA two pieces of cut units (per
- * query row d sums, the running maximum and the softmax denominator, fp32; 16
- * to 128 rows). At most about 20 MB. Returns 0 for unsupported shapes.
+ * per sequence, 16 per CTA), and for each CTA (at most one per SM) two pieces
+ * of cut units (128 rows, or 256 where a KV head has more than 128 query rows
+ * in a sequence: per row d sums, the running maximum and the softmax
+ * denominator, fp32). At most about 40 MB, whatever the lengths. With Nq = 1
+ * and H_q / H_kv in {1, 2, 4, 8}: kv2_decode_workspace_size's partials.
+ * Returns 0 for unsupported shapes.
  */
 size_t kv2_attention_cross_workspace_size(const kv2_cache* cache, int H_q, int Nq, int max_len);
 
@@ -458,12 +461,18 @@ size_t kv2_attention_cross_workspace_size(const kv2_cache* cache, int H_q, int N
  * keys fp16(code*s + fp16(z + centroid)), values fp16(code*s + z), queries
  * scaled per row by a power of two (exact), (qP) rounded to fp16,
  * probabilities fp16 against a running maximum that may trail the true one by
- * a factor of 2^7.
+ * a factor of 2^7. With Nq = 1 and H_q / H_kv in {1, 2, 4, 8}: the kernel and
+ * the arithmetic of kv2_attention_decode. A row's result depends on no other
+ * row; a query row that holds a NaN or an infinity gives NaN in its own row.
  * ws     : device workspace of kv2_attention_cross_workspace_size bytes, its
  *          first 32-bit word zeroed by the caller before the first use: the
  *          kernel sets it to 1 when one of its waits runs out of its budget
  *          (KV2_WAIT_BUDGET_CYCLES); rows it had not finished are then NaN.
  *          Calls that share a workspace must not overlap.
+ * Errors: KV2_ERR_INVALID_ARG (NULL or misaligned pointers, Nq < 0, H_q not a
+ * multiple of H_kv, a NaN or infinite sm_scale), KV2_ERR_UNSUPPORTED (r; more
+ * than 2^30 query rows, or Nq * (H_q/H_kv)^2 at or above 2^32), KV2_ERR_CAPACITY
+ * (max_len), KV2_ERR_WORKSPACE.
  */
 kv2_status kv2_attention_cross(const kv2_cache* cache, const int32_t* lens, int max_len, const uint16_t* Q,
                                const int32_t* q_lens, int Nq, int H_q, float sm_scale, void* out, int out_dtype,
@@ -472,8 +481,9 @@ kv2_status kv2_attention_cross(const kv2_cache* cache, const int32_t* lens, int 
 /*
  * Workspace for kv2_attention_shared, in bytes: as
  * kv2_attention_cross_workspace_size, plus every row's result over the prefix
- * and over its own cache (2 * B * H_q * (d + 2) fp32). Returns 0 for
- * unsupported shapes.
+ * and over its own cache (at most 2 * B * H_q * (d + 2) fp32), or instead of
+ * the latter kv2_decode_workspace_size's partials of the own caches where
+ * there are more of them than SMs. Returns 0 for unsupported shapes.
  */
 size_t kv2_attention_shared_workspace_size(const kv2_cache* prefix, const kv2_cache* cache, int H_q,
                                            int max_prefix_len, int max_len);
@@ -493,7 +503,9 @@ size_t kv2_attention_shared_workspace_size(const kv2_cache* prefix, const kv2_ca
  *          into 0..max_prefix_len and 0..max_len; NULL: the maximum each. A
  *          query with no token at all gives zeros.
  * Q, out : bf16 [B][H_q][d]; fp32 or bf16 [B][H_q][d].
- * Requirements, arithmetic, replay and ws: as kv2_attention_cross.
+ * Requirements, arithmetic, replay and ws: as kv2_attention_cross (where
+ * B * H_kv is more than the GPU's SMs and H_q / H_kv is 1, 2, 4 or 8, the own
+ * caches take kv2_attention_decode's kernel and arithmetic).
  * Errors: KV2_ERR_INVALID_ARG (cache->B not a multiple of prefix->B, different
  * H_kv or d, NULL or misaligned pointers), KV2_ERR_UNSUPPORTED (r),
  * KV2_ERR_CAPACITY (a maximum beyond its cache), KV2_ERR_WORKSPACE.

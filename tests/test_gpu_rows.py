@@ -158,6 +158,93 @@ def test_shared(i):
     plain.check(got, want, sigma, DT[dt], "shared")
 
 
+@pytest.mark.parametrize("B,H,G,Nq,r,fmt,dt", [(30, 4, 4, 80, 8, 0, 1), (100, 4, 3, 20, 16, 1, 0), (7, 12, 1, 400, 0, 0, 0)])
+def test_many_units_a_cta(B, H, G, Nq, r, fmt, dt):
+    """More row blocks than SMs, of several heads each: query rows, fragments of P and output rows change from unit to
+    unit in every CTA, and borders fall inside units."""
+    import bit_kv_cache_centroid_b200 as kv2
+    lens = [(53 * b) % 390 for b in range(B)]
+    ql = [(29 * b + 11) % (Nq + 1) for b in range(B)]
+    pc, P = packed(B, H, 128, 32, r, 400, fmt=fmt, seed=41, poison=lens)
+    c = device_cache(pc, P)
+    Q = queries((B, Nq, H * G, 128), 42, 0.8)
+    out = torch.full(Q.shape, 7.0, dtype=DT[dt], device="cuda")
+    got = kv2.kv2_attention_cross(c, ints(lens), Q.cuda(), 0.09, dt, q_lens=ints(ql), out=out).cpu()
+    want, sigma = cross_plain(pc, P, Q, lens, ql, 0.09)
+    for b in range(B):
+        plain.check(got[b, :ql[b]], want[b, :ql[b]], sigma[b, :ql[b]], DT[dt], f"sequence {b}")
+        assert (got[b, ql[b]:] == 7.0).all(), "rows behind the queries were written"
+
+
+@pytest.mark.parametrize("scale", [-0.09, 0.0])
+def test_negative_and_zero_scale(scale):
+    import bit_kv_cache_centroid_b200 as kv2
+    pc, P = packed(2, 2, 128, 16, 8, 256, seed=44)
+    c = device_cache(pc, P)
+    lens = [200, 77]
+    for Nq in (1, 9, 150):
+        Q = queries((2, Nq, 4, 128), 45 + Nq)
+        want, sigma = cross_plain(pc, P, Q, lens, [Nq] * 2, scale)
+        got = kv2.kv2_attention_cross(c, ints(lens), Q.cuda(), scale).cpu()
+        plain.check(got, want, sigma, torch.float32, f"{Nq} queries")
+    Q = queries((2, 4, 128), 46)
+    want, sigma = shared_plain(pc, pc, P, P, Q, lens, lens, scale)
+    plain.check(kv2.kv2_attention_shared(c, ints(lens), c, ints(lens), Q.cuda(), scale).cpu(), want, sigma, torch.float32, "shared")
+
+
+def test_no_tokens_at_all_gives_zeros():
+    import bit_kv_cache_centroid_b200 as kv2
+    pc, P = packed(2, 2, 64, 16, 8, 128, seed=47, poison=[0, 0])
+    c = device_cache(pc, P)
+    for Nq, G in ((1, 1), (1, 3), (5, 2), (200, 2)):
+        got = kv2.kv2_attention_cross(c, None, queries((2, Nq, 2 * G, 64), 48).cuda(), 0.125, max_len=0)
+        assert (got == 0).all()
+    got = kv2.kv2_attention_shared(c, None, c, None, queries((2, 4, 64), 49).cuda(), 0.125, max_prefix_len=0, max_len=0)
+    assert (got == 0).all()
+
+
+def test_two_calls_at_once_with_their_own_workspaces():
+    """Two streams, the same caches: each call gives what it gives alone."""
+    import bit_kv_cache_centroid_b200 as kv2
+    pc, P = packed(3, 4, 128, 64, 8, 2048, seed=51)
+    c = device_cache(pc, P)
+    Qs = [queries((3, n, 8, 128), n).cuda() for n in (40, 300)]
+    alone = [kv2.kv2_attention_cross(c, None, q, 0.09).clone() for q in Qs]
+    wss = [torch.zeros(kv2.kv2_attention_cross_workspace_size(c, 8, q.shape[1], 2048), dtype=torch.uint8, device="cuda") for q in Qs]
+    outs = [torch.empty(q.shape, device="cuda") for q in Qs]
+    streams = [torch.cuda.Stream() for _ in Qs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, ws, o, st in zip(Qs, wss, outs, streams):
+            with torch.cuda.stream(st):
+                kv2.kv2_attention_cross(c, None, q, 0.09, out=o, ws=ws)
+    torch.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        assert torch.equal(a, o)
+
+
+def test_a_call_on_a_given_stream_owns_its_workspace_there():
+    """Output and workspace of a call on another stream than the current one come from that stream's memory: what the
+    current stream allocates meanwhile does not fall on them."""
+    import bit_kv_cache_centroid_b200 as kv2
+    pc, P = packed(2, 4, 128, 64, 8, 2048, seed=53)
+    c = device_cache(pc, P)
+    Q = queries((2, 300, 8, 128), 54).cuda()
+    want = kv2.kv2_attention_cross(c, None, Q, 0.09)
+    side = torch.cuda.Stream()
+    size = kv2.kv2_attention_cross_workspace_size(c, 8, 300, 2048)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+        got.append(kv2.kv2_attention_cross(c, None, Q, 0.09, stream=side))
+        torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g, want)
+
+
 def test_shared_without_prefix_is_a_ragged_decode():
     """Prefix lengths of zero, and cross attention of one query: both the plain attention over the sequences' own
     caches. (The two take different kernels: one rounds reconstructed keys to fp16, 2^-11 of their size, the other does
