@@ -38,8 +38,9 @@
 // power of two, and p's rounding does not depend on where the work is cut.
 //
 // Warp roles of a CTA (one per SM): 8 softmax warps; 8 warps that dequantize
-// keys and 8 for values (the latter also load the unit's queries), so that the
-// waits and loads of one overlap the arithmetic of the other; one warp that
+// keys and 8 for values (they also load the unit's queries: all of them 256
+// rows, the value warps 128), so that the waits and loads of one overlap the
+// arithmetic of the other; one warp that
 // issues the MMAs, polling both groups; one thread that copies packed tiles to
 // shared memory. Registers are traded between the roles' warpgroups.
 //
@@ -52,6 +53,14 @@
 // Every wait is bounded by an SM-clock budget; on expiry the CTA's abort flag
 // ends the other waits, the workspace's first word is set, the rows of the
 // CTA's remaining part become NaN and the kernel ends.
+//
+// Measured on a B200 (cold caches): 4,680 queries x 4,096 keys x 40 heads 765 us,
+// 530 TFLOP/s, 0.32 of the bf16 GEMM rate; x 512 keys 152 us; 32 rows (8
+// continuations of 4 heads) over 32,768 shared keys 68 us. Bound: the softmax
+// and the hand-overs between the roles. A tile takes about 8,300 cycles for two
+// groups of 128 rows (softmax 4,000, of them 2,048 the exponentials; tensor core
+// 2,100) and 5,000 with up to 128 rows (keys 2,900), a unit 20,000 more for its
+// queries, first maxima and output rows.
 #include <algorithm>
 #include <cmath>
 
