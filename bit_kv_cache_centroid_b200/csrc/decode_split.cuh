@@ -254,7 +254,9 @@ struct DCfg {
 
 // Q8: the PSAC coefficients are int8 codes with a per-token fp16 scale
 // (cache format 1), else fp16 (format 0). GS: channels per scale/zero group.
-template <int D, int G, bool U16, bool Q8, int GS>
+// RAGGED: lengths from p.lens (a kernel of its own: the choice at run time cost
+// the long decode of 187,200 tokens x 40 heads 1.5 %)
+template <int D, int G, bool U16, bool Q8, int GS, bool RAGGED>
 __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
   using Cfg = DCfg<D, G, U16, GS>;
   using CL = Cols<G>;
@@ -280,11 +282,11 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
   const int b = bh / p.H_kv, h = bh % p.H_kv;
   const size_t base_slot = size_t(bh) * p.cap;
   const int t_begin = split * p.tiles_per_split * kTile;
-  const int len = p.lens ? min(max(p.lens[b], 0), p.len) : p.len;
+  const int len = RAGGED ? min(max(p.lens[b], 0), p.len) : p.len;
   const int t_end = min(len, t_begin + p.tiles_per_split * kTile);
   const int ntiles = (t_end > t_begin) ? (t_end - t_begin + kTile - 1) / kTile : 0;
 
-  if (p.lens && ntiles == 0) {
+  if (RAGGED && ntiles == 0) {
     // a split behind its sequence's end: nothing to merge
     asm volatile("griddepcontrol.launch_dependents;");
     float* dst = p.part + (size_t(bh) * p.splits + split) * G * (D + 2);
@@ -919,7 +921,8 @@ size_t split_smem(int M, int r) {
 template <int D, int G, bool U16, int GS>
 cudaError_t launch_split(const SplitParams& sp, int B, cudaStream_t s) {
   const size_t smem = split_smem<D, G, U16, GS>(sp.M, sp.r);
-  auto kern = sp.psac_fmt == 1 ? decode_split<D, G, U16, true, GS> : decode_split<D, G, U16, false, GS>;
+  auto kern = sp.psac_fmt == 1 ? (sp.lens ? decode_split<D, G, U16, true, GS, true> : decode_split<D, G, U16, true, GS, false>)
+                               : (sp.lens ? decode_split<D, G, U16, false, GS, true> : decode_split<D, G, U16, false, GS, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   dim3 grid(sp.splits, B * sp.H_kv);
@@ -957,7 +960,7 @@ cudaError_t launch_g(int G, const SplitParams& sp, int B, cudaStream_t s) {
 template <int D, int G, bool U16, int GS>
 int ctas_per_sm_t(int M, int r) {
   const size_t smem = split_smem<D, G, U16, GS>(M, r);
-  auto kern = decode_split<D, G, U16, false, GS>;
+  auto kern = decode_split<D, G, U16, false, GS, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return 4;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem) != cudaSuccess || n <= 0) return 4;

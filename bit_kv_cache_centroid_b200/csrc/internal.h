@@ -54,6 +54,7 @@ struct QuantizeArgs {
   const int* n_rows = nullptr;
 };
 cudaError_t launch_quantize(const QuantizeArgs& a, cudaStream_t s);
+cudaError_t launch_quantize_rows(const QuantizeArgs& a, cudaStream_t s);   // a.rows, a.n_rows
 
 // Append with the position rotation applied on the way, at per-sequence places.
 struct RotaryArgs {

@@ -11,7 +11,7 @@
 // Two kernels. rotate_rows: one block per token of the padded batch turns the
 // token's keys (to the workspace, tokens in use packed together) and queries,
 // codes its values into the cache, and notes where the token goes; quantize_kernel
-// (quantize.cu), its programmatic dependent, then quantizes the packed keys as
+// (quantize.cuh), its programmatic dependent, then quantizes the packed keys as
 // every append does. Tokens behind a sequence's count cost an empty block.
 //
 // Bound: memory; per token and KV head 256 B of key read, 256 B written and
@@ -239,7 +239,7 @@ cudaError_t launch_rotary(const RotaryArgs& a, const QuantizeArgs& q, cudaStream
   k.V = nullptr;
   k.rows = p.rows;
   k.n_rows = p.n_rows;
-  return launch_quantize(k, s);
+  return launch_quantize_rows(k, s);
 }
 
 }  // namespace kv2
