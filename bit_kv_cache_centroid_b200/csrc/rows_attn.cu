@@ -56,7 +56,7 @@
 //
 // Measured on a B200 (cold caches): 4,680 queries x 4,096 keys x 40 heads 765 us,
 // 530 TFLOP/s, 0.32 of the bf16 GEMM rate; x 512 keys 152 us; 32 rows (8
-// continuations of 4 heads) over 32,768 shared keys 68 us. Bound: the softmax
+// continuations of 4 heads) over 32,768 shared keys 64 us. Bound: the softmax
 // and the hand-overs between the roles. A tile takes about 8,300 cycles for two
 // groups of 128 rows (softmax 4,000, of them 2,048 the exponentials; tensor core
 // 2,100) and 5,000 with up to 128 rows (keys 2,900), a unit 20,000 more for its
@@ -134,10 +134,12 @@ struct RCfg {
   // registers per thread by role, in all the launch's threads times kRegs
   static constexpr int kRegs = 72, kRegsSoft = 88, kRegsProd = 64, kRegsIssue = 72;
   static_assert(SW * kRegsSoft + 2 * PW * kRegsProd + 4 * kRegsIssue <= (SW + 2 * PW + 4) * kRegs, "register split");
-  // stages of keys, values and packed tiles. With WIDE units the keys of tile
-  // t + 1 are multiplied after P . V of tile t, a softmax later than they could
-  // first be written: one stage is enough.
-  static constexpr int KS = WIDE ? 1 : 2, VS = WIDE ? 1 : 2, RS = WIDE ? 3 : 2;
+  // stages of keys, values and packed tiles. One of keys is enough: with WIDE
+  // units the keys of tile t + 1 are multiplied a softmax after they could first
+  // be written, else the scores' columns are free as late. A third packed tile
+  // hides the copies' latency instead (up to 128 rows over 32,768 keys: 59 us
+  // against 64 us with two stages of keys and two packed tiles).
+  static constexpr int KS = 1, VS = WIDE ? 1 : 2, RS = 3;
   // packed tile: codes of keys and values, scale and zero words, ids, PSAC
   // (fp16, or int8 codes and from RAW_PSC on the tokens' scales)
   static constexpr int RAW_VC = kKeys * D / 4, RAW_KZ = 2 * RAW_VC, RAW_VZ = RAW_KZ + kKeys * D / 8;
