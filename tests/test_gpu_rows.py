@@ -223,6 +223,38 @@ def test_two_calls_at_once_with_their_own_workspaces():
         assert torch.equal(a, o)
 
 
+def test_one_workspace_for_calls_in_sequence():
+    """Calls of different kinds and sizes, one after another on one workspace and stream: each gives what it gives
+    alone, and the rotary append between them too."""
+    import bit_kv_cache_centroid_b200 as kv2
+    pc, P = packed(80, 2, 128, 16, 8, 272, seed=61)
+    pre, P0 = packed(2, 2, 128, 16, 8, 1024, seed=62)
+    c, cp = device_cache(pc, P), device_cache(pre, P0)
+    Qs, Qw, Qd = (queries(x, 63, 0.8).cuda() for x in ((80, 8, 128), (2, 200, 8, 128), (2, 1, 8, 128)))
+    ls = ints([(13 * k) % 250 for k in range(80)])
+    rot = kv2.Rotary(torch.randn(512, 128, generator=torch.Generator().manual_seed(1)).cuda())
+    K, V = (queries((80, 1, 2, 128), n).cuda() for n in (64, 65))
+    place = ints([260] * 80)
+    Q = Qs.unsqueeze(1).contiguous()
+    calls = [lambda ws: kv2.kv2_attention_cross(cp, None, Qw, 0.09, ws=ws),
+             lambda ws: kv2.kv2_rotary_append(c, rot, K, V, place.view(80, 1), place, 4, Q=Q, ws=ws),
+             lambda ws: kv2.kv2_attention_shared(cp, None, c, ls, Qs, 0.09, ws=ws),
+             lambda ws: kv2.kv2_attention_cross(cp, None, Qd, 0.09, ws=ws),
+             lambda ws: kv2.kv2_attention_cross(c, ls, Q, 0.09, ws=ws)]
+    size = max(kv2.kv2_attention_cross_workspace_size(cp, 8, 200, 1024), kv2.kv2_rotary_append_workspace_size(c, 1),
+               kv2.kv2_attention_shared_workspace_size(cp, c, 8, 1024, 272), kv2.kv2_attention_cross_workspace_size(c, 8, 1, 272))
+    alone = []
+    for f in calls:
+        alone.append(f(None))
+        torch.cuda.synchronize()
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    got = [f(ws) for _ in range(4) for f in calls]
+    torch.cuda.synchronize()
+    assert ws[:4].view(torch.int32).item() == 0
+    for i, g in enumerate(got):
+        assert torch.equal(g, alone[i % len(calls)]), f"call {i}"
+
+
 def test_a_call_on_a_given_stream_owns_its_workspace_there():
     """Output and workspace of a call on another stream than the current one come from that stream's memory: what the
     current stream allocates meanwhile does not fall on them."""
