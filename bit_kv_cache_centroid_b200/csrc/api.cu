@@ -421,11 +421,8 @@ kv2_status check_rows_io(const char* what, const uint16_t* Q, const void* out, i
   return KV2_OK;
 }
 
-// rows are ints in the kernel, and it divides them by G with 32-bit products
-bool rows_too_many(const kv2_cache* c, int H_q, long long Nq) {
-  const long long G = H_q / c->H_kv;
-  return Nq * H_q > (1ll << 30) / c->B || Nq * G * G >= (1ll << 32);
-}
+// rows are ints in the kernel
+bool rows_too_many(const kv2_cache* c, int H_q, long long Nq) { return Nq * H_q > (1ll << 30) / c->B; }
 
 kv2::RowsArgs cross_args(const kv2_cache* c, const int32_t* lens, int max_len, const int32_t* q_lens, int Nq, int H_q) {
   kv2::RowsArgs a{};

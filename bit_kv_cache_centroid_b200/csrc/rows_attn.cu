@@ -68,6 +68,7 @@
 #include "internal.h"
 #include "mbarrier.cuh"
 #include "packed_tile.cuh"
+#include "row_division.h"
 #include "umma.cuh"
 
 namespace kv2 {
@@ -101,9 +102,8 @@ struct RowsSource {
 struct RowsParams {
   RowsSource src[2];
   int nsrc, H_kv, H_q;
-  uint32_t g_inv;           // ceil(2^32 / G), G = H_q / H_kv > 1 (G = 1: 0)
-  // row / G, for row * G < 2^32
-  __device__ int per_head(int row) const { return g_inv ? int(__umulhi(uint32_t(row), g_inv)) : row; }
+  RowDivision by_group;     // by G = H_q / H_kv
+  __device__ int per_head(int row) const { return int(by_group(uint32_t(row))); }
   const uint16_t* Q;        // bf16 [rows of (b, i)][H_q][D]
   void* out;                // null: whole units go to dir_o / dir_ml
   int out_dtype;
@@ -1423,8 +1423,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
   p.nsrc = pl.listed;
   p.H_kv = a.src[0].c->H_kv;
   p.H_q = a.H_q;
-  const uint32_t G = uint32_t(a.H_q / p.H_kv);
-  p.g_inv = G > 1 ? uint32_t(((1ull << 32) + G - 1) / G) : 0;
+  p.by_group = row_division(uint32_t(a.H_q / p.H_kv));
   p.Q = a.Q;
   p.out = a.out;
   p.out_dtype = a.out_dtype;
