@@ -53,8 +53,10 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
 }
 
 // Host side: the wait budget in SM clock cycles (KV2_WAIT_BUDGET_CYCLES,
-// default 2^31, about one second), and KV2_FORCE_WAIT_TIMEOUT=1, under which
-// kernels wait on a barrier that nothing completes (tests of the timeout path).
+// default 2^31, about one second), and the tests' switches of the timeout path:
+// KV2_FORCE_WAIT_TIMEOUT=1, under which kernels wait on a barrier that nothing
+// completes, and KV2_FORCE_WAIT_TIMEOUT_CTA=c, under which one CTA alone of the
+// row attention kernel gives up.
 inline unsigned long long env_wait_budget() {
   const char* e = std::getenv("KV2_WAIT_BUDGET_CYCLES");
   return e ? std::strtoull(e, nullptr, 10) : (1ull << 31);
@@ -62,6 +64,13 @@ inline unsigned long long env_wait_budget() {
 inline int env_force_timeout() {
   const char* e = std::getenv("KV2_FORCE_WAIT_TIMEOUT");
   return (e && e[0] == '1') ? 1 : 0;
+}
+// 0: none, 1: every CTA, 2 + c: CTA c alone
+inline int env_force_timeout_ctas() {
+  if (env_force_timeout()) return 1;
+  const char* e = std::getenv("KV2_FORCE_WAIT_TIMEOUT_CTA");
+  const long c = e ? std::strtol(e, nullptr, 10) : -1;
+  return c >= 0 && c < (1l << 30) ? 2 + int(c) : 0;
 }
 
 }  // namespace kv2

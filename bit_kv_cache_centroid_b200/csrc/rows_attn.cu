@@ -52,7 +52,13 @@
 //
 // Every wait is bounded by an SM-clock budget; on expiry the CTA's abort flag
 // ends the other waits, the workspace's first word is set, the rows of the
-// CTA's remaining part become NaN and the kernel ends.
+// CTA's remaining part become NaN and the kernel ends. No row is finished from
+// operands that are not there: producers whose wait failed go on over whatever
+// their stages hold, but only after the flag is up, and a unit's rows are
+// written as numbers only where the flag is still down after the wait for
+// their last product; the next product that starts on the same columns waits
+// for the softmax warps of the group, which arrive no more once their own wait
+// has failed.
 //
 // Measured on a B200 (cold caches): 4,680 queries x 4,096 keys x 40 heads 765 us,
 // 530 TFLOP/s, 0.32 of the bf16 GEMM rate; x 512 keys 152 us; 32 rows (8
@@ -82,6 +88,7 @@ constexpr float kTrail = 7.0f;         // a score this far above the running max
 // query rows, first maxima and output rows take about as long as that many key
 // tiles, so parts with many short units get fewer tiles.
 constexpr int kLead = 2;
+constexpr int kForceTile = 4;
 
 struct RowsSource {
   const uint32_t* k_code;
@@ -121,7 +128,7 @@ struct RowsParams {
   int splits;
   uint32_t none;            // 0 (see the producers' release of a packed tile)
   unsigned long long budget;
-  int force_timeout;
+  int force_timeout;        // tests: 1 every CTA's first wait expires, 2 + c: CTA c's wait for its packed tile kForceTile
 };
 
 // D channels; WIDE: units of 256 rows, else of 128
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
     int scores = 0;                               // tiles whose scores are issued (by the only group that takes them)
     unsigned long long since = clock64();
     bool ok = true;
-    if (p.force_timeout) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar + B_NEVER, 0, p.budget, abort));
+    if (p.force_timeout == 1) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar + B_NEVER, 0, p.budget, abort));
     while (ok && (cur[0].cnt || cur[1].cnt)) {
       bool moved = false;
 #pragma unroll
@@ -548,6 +555,11 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
         for (int jj = 0; jj < cnt; ++jj, ++t) {
           const int st = t % Cfg::RS, tok = (w.j + jj) * kKeys;
           if (t >= Cfg::RS && !mbar_wait_or_abort(bar + B_REMPTY + 8 * st, (t / Cfg::RS - 1) & 1, p.budget, abort)) {
+            out = true;
+            break;
+          }
+          if (t == kForceTile && p.force_timeout == 2 + int(blockIdx.x)) {
+            *abort = 1;
             out = true;
             break;
           }
@@ -873,7 +885,8 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
     const uint32_t lane_base = uint32_t(wq * 32) << 16;
     const uint32_t tS = tmem + x * kKeys + lane_base, tO = tmem + 2 * kKeys + x * kRows + lane_base;
     float2* ml_s = reinterpret_cast<float2*>(smem + Cfg::OFF_ML);
-    bool dead = false;                            // a wait ran out
+    // a wait of the lane ran out, or before the last vote one of the warp (below, of both groups)
+    bool dead = false;
     int t0 = 0, seg = 0, k = 0;                   // the part's first tile; tiles of this group
     for (; w.more(); w.next(p), ++seg) {
       const RowsSource& s = p.src[w.src];
@@ -965,11 +978,15 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
           l += (s01.x + s23.x) + (s01.y + s23.y);
         }
         fence_before_sync();
+        // (the lanes of a wait that failed have spoilt rows of this warp alone)
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + B_PFULL + 8 * x);
       }
       // ---- the unit's rows: a group's 128 rows, or half their channels of both groups' sums
-      if (jx < cnt) dead |= !mbar_wait_or_abort(bar + B_PDONE + 8 * x, (k - 1) & 1, p.budget, abort);
+      if (jx < cnt && !dead) dead = !mbar_wait_or_abort(bar + B_PDONE + 8 * x, (k - 1) & 1, p.budget, abort);
+      dead = __any_sync(0xffffffffu, dead || *abort);
       fence_after_sync();
       float f0 = 1.0f, f1 = 0.0f;
       if constexpr (!WIDE) {
@@ -1472,8 +1489,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
     const cudaError_t e = launch_decode_split(d, part, s);
     if (e != cudaSuccess) return e;
   }
-  p.force_timeout = env_force_timeout();
-  p.budget = p.force_timeout ? (1ull << 20) : env_wait_budget();
+  p.force_timeout = env_force_timeout_ctas();
+  p.budget = p.force_timeout == 1 ? (1ull << 20) : env_wait_budget();
   return a.src[0].c->d == 64 ? launch_d<64>(p, pl, s) : launch_d<128>(p, pl, s);
 }
 
