@@ -28,19 +28,20 @@ __global__ void decode_combine(const float* __restrict__ part, int H_q, int H_kv
   float m = -FLT_MAX;
   for (int s0 = 0; s0 < splits; s0 += 32) {
     const int sp = s0 + lane;
-    if (sp < splits && base[sp * sstride + D + 1] > 0.0f) m = fmaxf(m, base[sp * sstride + D]);
+    if (sp < splits && base[sp * sstride + D + 1] != 0.0f) m = fmaxf(m, base[sp * sstride + D]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   // weights 2^(m_s - m) per split (0 for an empty split), shared by shuffles;
-  // the channel sums' loads are independent of one another
+  // the channel sums' loads are independent of one another. A sum that is not a
+  // number (a query with a NaN, a wait that ran out) makes the row NaN.
   float o = 0.0f, l = 0.0f;
   for (int s0 = 0; s0 < splits; s0 += 32) {
     const int sp = s0 + lane;
     float f = 0.0f;
     if (sp < splits) {
       const float ls = base[sp * sstride + D + 1];
-      if (ls > 0.0f) {
+      if (ls != 0.0f) {
         f = exp2f(base[sp * sstride + D] - m);
         l = fmaf(f, ls, l);
       }
@@ -52,7 +53,7 @@ __global__ void decode_combine(const float* __restrict__ part, int H_q, int H_kv
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-  const float v = (l > 0.0f) ? o / l : 0.0f;
+  const float v = (l == 0.0f) ? 0.0f : o / l;
   if (out_dtype == KV2_OUT_F32) static_cast<float*>(out)[size_t(bq) * D + c] = v;
   else static_cast<__nv_bfloat16*>(out)[size_t(bq) * D + c] = __float2bfloat16_rn(v);
 }
