@@ -131,7 +131,7 @@ cudaError_t launch_decode_split(const DecodeArgs& a, float* part, cudaStream_t s
   const kv2_cache& c = *a.c;
   int splits, tps;
   plan_splits(c, a.H_q, a.len, &splits, &tps);
-  const int force = env_force_timeout();
+  const int force = env_force_timeout_ctas();
   SplitParams sp{c.k_code, c.v_code, c.k_sz, c.v_sz, c.cidx, c.psac,
                  static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(c.centroids), c.P,
                  a.sm_scale * kLog2e, part, static_cast<int*>(a.ws),

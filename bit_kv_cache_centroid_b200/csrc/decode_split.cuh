@@ -75,7 +75,7 @@ struct SplitParams {
   float* part;            // [B*H_kv][splits][G][D + 2]
   int* err;               // sticky error word: 1 after a wait ran out of its budget
   unsigned long long budget;   // SM clock cycles a wait may take
-  int force_timeout;      // wait on copies that are never issued (tests)
+  int force_timeout;      // tests: 1 every CTA, 2 + c: CTA c alone waits on copies that are never issued
   int wait_from;          // first slot the preceding (primary) kernel writes
   int H_kv, H_q, M, r, cap, len, splits, tiles_per_split;
   int psac_fmt;                 // 0: fp16 coefficients; 1: int8 codes + fp16 scale per token
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
   int issued = 0;                                        // tiles issued (thread 0)
   bool dep_done = false;                                 // primary grid waited for (thread 0)
   auto issue = [&](int tile) {
-    if (tile >= ntiles || p.force_timeout) return;
+    if (tile >= ntiles || p.force_timeout == 1 || p.force_timeout == 2 + bh * p.splits + split) return;
     const int st = tile % kStages;
     const uint32_t dst = smem_u32(smem + st * stage);
     const uint32_t bar = bar0 + 8 * st;
@@ -860,10 +860,9 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
       for (int j = tile; j < issued; ++j) mbar_wait(bar0 + 8 * (j % kStages), (j / kStages) & 1, p.budget);
     }
     float* dst = p.part + (size_t(bh) * p.splits + split) * G * (D + 2);
-    for (int i = tid; i < G * (D + 2); i += kThreads) {
-      const int c = i % (D + 2);
-      dst[i] = (c == D + 1) ? 1.0f : (c == D ? 0.0f : __int_as_float(0x7fc00000));
-    }
+    // (the sum too: it reaches the merged row whatever the weight of this split)
+    for (int i = tid; i < G * (D + 2); i += kThreads)
+      dst[i] = i % (D + 2) == D ? 0.0f : __int_as_float(0x7fc00000);
     return;
   }
   __syncthreads();

@@ -56,7 +56,7 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
 // default 2^31, about one second), and the tests' switches of the timeout path:
 // KV2_FORCE_WAIT_TIMEOUT=1, under which kernels wait on a barrier that nothing
 // completes, and KV2_FORCE_WAIT_TIMEOUT_CTA=c, under which one CTA alone of the
-// row attention kernel gives up.
+// row attention and split decode kernels gives up.
 inline unsigned long long env_wait_budget() {
   const char* e = std::getenv("KV2_WAIT_BUDGET_CYCLES");
   return e ? std::strtoull(e, nullptr, 10) : (1ull << 31);

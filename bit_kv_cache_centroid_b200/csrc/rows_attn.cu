@@ -1001,8 +1001,10 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
       }
       const bool whole = j0 == 0 && cnt == tiles_of(len);
       if (dead) {
+        // (a sum that is not a number reaches the merged row whatever the weight of
+        // its piece; channels alone are not looked at where the weight is 0)
         m = 0.0f;
-        l = 1.0f;
+        l = __int_as_float(0x7fc00000);
       }
       if (warp_ok) {
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);

@@ -69,3 +69,74 @@ def test_one_cta_gives_up(monkeypatch, B, H, G, Nq, length, d):
             assert torch.equal(got[~bad], good[~bad]), "rows that were finished differ"
             assert torch.equal(call(), good)
     assert reached
+
+
+def err(ws):
+    return ws[:4].view(torch.int32).item()
+
+
+@pytest.mark.parametrize("Nq", [1, 20, 300])
+def test_a_lost_piece_is_not_outweighed(monkeypatch, Nq):
+    """One unit in pieces over all CTAs, scores of some hundred: the piece that was given up makes its rows NaN, however
+    large the other pieces' maxima."""
+    import bit_kv_cache_centroid_b200 as kv2
+    length = 128 * 1000
+    pc, P = packed(1, 1, 128, 64, 8, length, seed=35)
+    c = device_cache(pc, P)
+    G = 3 if Nq == 1 else 1                                        # (three heads: the row kernel)
+    Q = queries((1, Nq, G, 128), 36, 30.0).cuda()
+    ws = torch.zeros(kv2.kv2_attention_cross_workspace_size(c, G, Nq, length), dtype=torch.uint8, device="cuda")
+    assert torch.isfinite(kv2.kv2_attention_cross(c, None, Q, 0.09, ws=ws)).all() and err(ws) == 0
+    for cta in (0, 70, 147):
+        if not any(nan for _, nan in parts_of_cta(cta, 1, Nq, G, 1, length)):
+            continue
+        monkeypatch.setenv("KV2_FORCE_WAIT_TIMEOUT_CTA", str(cta))
+        got = kv2.kv2_attention_cross(c, None, Q, 0.09, ws=ws)
+        monkeypatch.delenv("KV2_FORCE_WAIT_TIMEOUT_CTA")
+        assert err(ws) == 1
+        ws[:4].zero_()
+        lost = {r for (_, _, r0, n), nan in parts_of_cta(cta, 1, Nq, G, 1, length) if nan for r in range(r0, r0 + n)}
+        for r in lost:
+            assert torch.isnan(got[0, r // G, r % G]).all(), (cta, r)
+
+
+def test_a_lost_split_of_an_own_cache_is_not_outweighed(monkeypatch):
+    """More own caches than SMs, one CTA of the split decode kernel gives up: its pair's rows are NaN beside a prefix of
+    far larger scores, all other rows as they are without."""
+    import bit_kv_cache_centroid_b200 as kv2
+    B, H, G, d = 100, 2, 2, 128
+    pre, P0 = packed(1, H, d, 64, 8, 128, seed=37)
+    pc, P = packed(B, H, d, 64, 8, 400, seed=38)
+    pre.k_sz[:] = pre.k_sz & 0xFFFF0000 | 0x5640                   # scales of 100: scores far above the own caches'
+    cp, c = device_cache(pre, P0), device_cache(pc, P)
+    Q = queries((B, H * G, d), 39, 8.0).cuda()
+    ws = torch.zeros(kv2.kv2_attention_shared_workspace_size(cp, c, H * G, 128, 400), dtype=torch.uint8, device="cuda")
+    call = lambda: kv2.kv2_attention_shared(cp, None, c, None, Q, 0.09, ws=ws)
+    good = call()
+    assert torch.isfinite(good).all() and err(ws) == 0
+    for cta in (0, 61, 199):
+        monkeypatch.setenv("KV2_FORCE_WAIT_TIMEOUT_CTA", str(cta))
+        got = call()
+        monkeypatch.delenv("KV2_FORCE_WAIT_TIMEOUT_CTA")
+        assert err(ws) == 1
+        ws[:4].zero_()
+        bad = torch.isnan(got).all(-1)
+        assert torch.equal(bad, torch.isnan(got).any(-1))
+        hit = bad.nonzero()
+        assert len(hit) == G and len({(b, h // G) for b, h in hit.tolist()}) == 1, hit
+        assert torch.equal(got[~bad], good[~bad])
+
+
+def test_a_lost_split_of_one_query(monkeypatch):
+    import bit_kv_cache_centroid_b200 as kv2
+    pc, P = packed(2, 2, 128, 64, 8, 20000, seed=40)
+    c = device_cache(pc, P)
+    Q = queries((2, 1, 8, 128), 41, 30.0).cuda()
+    ws = torch.zeros(kv2.kv2_attention_cross_workspace_size(c, 8, 1, 20000), dtype=torch.uint8, device="cuda")
+    good = kv2.kv2_attention_cross(c, None, Q, 0.09, ws=ws)
+    assert torch.isfinite(good).all() and err(ws) == 0
+    monkeypatch.setenv("KV2_FORCE_WAIT_TIMEOUT_CTA", "1")
+    got = kv2.kv2_attention_cross(c, None, Q, 0.09, ws=ws)
+    monkeypatch.delenv("KV2_FORCE_WAIT_TIMEOUT_CTA")
+    assert err(ws) == 1 and torch.isnan(got[0, 0, :4]).all()
+    assert torch.equal(got[0, 0, 4:], good[0, 0, 4:]) and torch.equal(got[1], good[1])
