@@ -476,6 +476,7 @@ kv2_status kv2_attention_cross(const kv2_cache* c, const int32_t* lens, int max_
   if (st != KV2_OK) return st;
   if (cross_is_decode(c, H_q, Nq)) {
     kv2::DecodeArgs d{c, max_len, H_q, Q, sm_scale, out, out_dtype, ws, ws_bytes};
+    d.rows = true;
     d.lens = lens;
     d.q_lens = q_lens;
     return cuda_status(kv2::launch_decode(d, static_cast<cudaStream_t>(stream)), "cross launch");

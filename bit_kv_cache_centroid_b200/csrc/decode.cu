@@ -131,13 +131,13 @@ cudaError_t launch_decode_split(const DecodeArgs& a, float* part, cudaStream_t s
   const kv2_cache& c = *a.c;
   int splits, tps;
   plan_splits(c, a.H_q, a.len, &splits, &tps);
-  const int force = env_force_timeout_ctas();
+  const int force = a.rows ? env_force_timeout_ctas() : env_force_timeout();
   SplitParams sp{c.k_code, c.v_code, c.k_sz, c.v_sz, c.cidx, c.psac,
                  static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(c.centroids), c.P,
                  a.sm_scale * kLog2e, part, static_cast<int*>(a.ws),
                  force ? (1ull << 20) : env_wait_budget(), force, a.wait_from,
                  c.H_kv, a.H_q, c.M, c.r, c.capacity, a.len, splits, tps, c.psac_fmt, c.psac_scale,
-                 c.block_table, c.page_tokens, a.lens};
+                 c.block_table, c.page_tokens, a.lens, a.rows};
   const int G = a.H_q / c.H_kv;
   switch (cache_group(c)) {
     case 32: return launch_gs<32>(c, G, sp, s);

@@ -75,14 +75,15 @@ struct SplitParams {
   float* part;            // [B*H_kv][splits][G][D + 2]
   int* err;               // sticky error word: 1 after a wait ran out of its budget
   unsigned long long budget;   // SM clock cycles a wait may take
-  int force_timeout;      // tests: 1 every CTA, 2 + c: CTA c alone waits on copies that are never issued
+  int force_timeout;      // tests: 1 every CTA, 2 + c (ROWS): CTA c alone waits on copies that are never issued
   int wait_from;          // first slot the preceding (primary) kernel writes
   int H_kv, H_q, M, r, cap, len, splits, tiles_per_split;
   int psac_fmt;                 // 0: fp16 coefficients; 1: int8 codes + fp16 scale per token
   const uint16_t* psac_scale;
   const int32_t* table;         // paged cache: block table [B][cap / page] (null: contiguous)
   int page;
-  const int32_t* lens;          // tokens per sequence, device [B], taken into 0..len (null: len each)
+  const int32_t* lens;          // ROWS kernels: tokens per sequence, device [B], taken into 0..len (null: len each)
+  bool rows;                    // host: the ROWS kernel
 };
 
 // d = a * b + c on two fp16 lanes
@@ -254,10 +255,14 @@ struct DCfg {
 
 // Q8: the PSAC coefficients are int8 codes with a per-token fp16 scale
 // (cache format 1), else fp16 (format 0). GS: channels per scale/zero group.
-// RAGGED: lengths from p.lens (a kernel of its own: the choice at run time cost
-// the long decode of 187,200 tokens x 40 heads 1.5 %)
-template <int D, int G, bool U16, bool Q8, int GS, bool RAGGED>
-__global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
+// ROWS: the kernel of cross attention and shared prefixes, with lengths from
+// p.lens and every head's query scaled by itself, so that a head that is huge or
+// not finite leaves its group's others alone (a kernel of its own: the choice of
+// lengths at run time cost the long decode of 187,200 tokens x 40 heads 1.5 %).
+// One head a group (ROWS) is held to 80 registers, where it would take 83 and
+// lose the sixth CTA an SM.
+template <int D, int G, bool U16, bool Q8, int GS, bool ROWS>
+__global__ void __launch_bounds__(kThreads, ROWS && G == 1 ? 6 : 0) decode_split(SplitParams p) {
   using Cfg = DCfg<D, G, U16, GS>;
   using CL = Cols<G>;
   constexpr int NG = Cfg::NG, NW = Cfg::NW, NT = Cfg::NT, NCOL = Cfg::NCOL;
@@ -282,11 +287,11 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
   const int b = bh / p.H_kv, h = bh % p.H_kv;
   const size_t base_slot = size_t(bh) * p.cap;
   const int t_begin = split * p.tiles_per_split * kTile;
-  const int len = RAGGED ? min(max(p.lens[b], 0), p.len) : p.len;
+  const int len = ROWS && p.lens ? min(max(p.lens[b], 0), p.len) : p.len;
   const int t_end = min(len, t_begin + p.tiles_per_split * kTile);
   const int ntiles = (t_end > t_begin) ? (t_end - t_begin + kTile - 1) / kTile : 0;
 
-  if (RAGGED && ntiles == 0) {
+  if (ROWS && ntiles == 0) {
     // a split behind its sequence's end: nothing to merge
     asm volatile("griddepcontrol.launch_dependents;");
     float* dst = p.part + (size_t(bh) * p.splits + split) * G * (D + 2);
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
   int issued = 0;                                        // tiles issued (thread 0)
   bool dep_done = false;                                 // primary grid waited for (thread 0)
   auto issue = [&](int tile) {
-    if (tile >= ntiles || p.force_timeout == 1 || p.force_timeout == 2 + bh * p.splits + split) return;
+    if (tile >= ntiles || (ROWS ? p.force_timeout == 1 || p.force_timeout == 2 + bh * p.splits + split : p.force_timeout)) return;
     const int st = tile % kStages;
     const uint32_t dst = smem_u32(smem + st * stage);
     const uint32_t bar = bar0 + 8 * st;
@@ -395,33 +400,75 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
   }
   __syncthreads();           // sgs and us are complete
   // scales for the tensor cores: max |q| 2^eq below 2^15 and
-  // max(|sigma|, |u|) 2^ea below 2^14
-  float qmax = 0.0f, amax = 0.0f;
-  for (int i = tid; i < G * D; i += kThreads) qmax = fmaxf(qmax, fabsf(qs[i]));
-  for (int i = tid; i < G * NG; i += kThreads) amax = fmaxf(amax, fabsf(sgs[i]));
-  for (int i = tid; i < G * r; i += kThreads) amax = fmaxf(amax, fabsf(us[i]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  }
-  if (lane == 0) {
-    red[kWarps * G + warp] = qmax;
-    red[kWarps * G + kWarps + warp] = amax;
-  }
-  __syncthreads();
-  const float* rq = red + kWarps * G;
-  qmax = fmaxf(fmaxf(rq[0], rq[1]), fmaxf(rq[2], rq[3]));
-  amax = fmaxf(fmaxf(rq[4], rq[5]), fmaxf(rq[6], rq[7]));
-  int qexp = 0, aexp = 0;
-  frexpf(qmax, &qexp);
-  frexpf(amax, &aexp);
-  const int eq = (qmax > 0.0f) ? 15 - qexp : 0;
-  const int ea = (amax > 0.0f) ? 14 - aexp : 0;
+  // max(|sigma|, |u|) 2^ea below 2^14, over the group's heads or (ROWS) of each.
   // q enters q.k as the integer rint(q qmul), |.| <= 127 * 256 (two signed
   // 8-bit digits); qinv = 1 / qmul rounded to fp32
-  const float qmul = ldexpf(127.0f / 128.0f, eq), qinv = 1.0f / qmul;
-  const float amul = ldexpf(1.0f, ea), ainv = ldexpf(1.0f, -ea);
+  constexpr bool APART = ROWS && G > 1;
+  constexpr int SC = APART ? NT : 1;
+  float qinv[SC], ainv[SC];                   // of this lane's columns in q.k
+  float qmul_all = 0.0f, amul_all = 0.0f;
+  if constexpr (APART) {
+    for (int g = warp; g < G; g += kWarps) {
+      float qm = 0.0f, am = 0.0f;
+      for (int i = lane; i < D; i += 32) qm = fmaxf(qm, fabsf(qs[g * D + i]));
+      for (int i = lane; i < NG; i += 32) am = fmaxf(am, fabsf(sgs[g * NG + i]));
+      for (int i = lane; i < r; i += 32) am = fmaxf(am, fabsf(us[g * r + i]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, o));
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+      }
+      if (lane == 0) {
+        int qe = 0, ae = 0;
+        frexpf(qm, &qe);
+        frexpf(am, &ae);
+        // (exponents kept where the powers are finite; an infinite query's row is
+        // NaN: its qinv is infinite and its integers 0)
+        red[g] = qm < INFINITY ? ldexpf(127.0f / 128.0f, qm > 0.0f ? min(15 - qe, 120) : 0) : 0.0f;
+        red[G + g] = ldexpf(1.0f, am > 0.0f && am < INFINITY ? min(14 - ae, 120) : 0);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < SC; ++nt) {
+      const int hd = min(4 * nt + tig, G - 1);
+      qinv[nt] = 1.0f / red[hd];
+      ainv[nt] = 1.0f / red[G + hd];          // (a power of two: exact)
+    }
+  } else {
+    float qmax = 0.0f, amax = 0.0f;
+    for (int i = tid; i < G * D; i += kThreads) qmax = fmaxf(qmax, fabsf(qs[i]));
+    for (int i = tid; i < G * NG; i += kThreads) amax = fmaxf(amax, fabsf(sgs[i]));
+    for (int i = tid; i < G * r; i += kThreads) amax = fmaxf(amax, fabsf(us[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    }
+    if (lane == 0) {
+      red[kWarps * G + warp] = qmax;
+      red[kWarps * G + kWarps + warp] = amax;
+    }
+    __syncthreads();
+    const float* rq = red + kWarps * G;
+    qmax = fmaxf(fmaxf(rq[0], rq[1]), fmaxf(rq[2], rq[3]));
+    amax = fmaxf(fmaxf(rq[4], rq[5]), fmaxf(rq[6], rq[7]));
+    if constexpr (ROWS) {                     // (2^eq and 2^ea stay finite)
+      qmax = fmaxf(qmax, 0x1p-100f);
+      amax = fmaxf(amax, 0x1p-100f);
+    }
+    int qexp = 0, aexp = 0;
+    frexpf(qmax, &qexp);
+    frexpf(amax, &aexp);
+    const int eq = (qmax > 0.0f) ? 15 - qexp : 0;
+    const int ea = (amax > 0.0f) ? 14 - aexp : 0;
+    qmul_all = ldexpf(127.0f / 128.0f, eq);
+    qinv[0] = 1.0f / qmul_all;
+    amul_all = ldexpf(1.0f, ea);
+    ainv[0] = ldexpf(1.0f, -ea);
+  }
+  auto qmul = [&](int hd) { return APART ? red[hd] : qmul_all; };
+  auto amul = [&](int hd) { return APART ? red[G + hd] : amul_all; };
   // B fragments of the zero-point / PSAC k-steps: aux column c is sigma_c
   // (c < NG), zero (c = NG when NG is odd), u_(c-NGP) (c - NGP < r), zero
   // beyond
@@ -438,7 +485,7 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
       float v = 0.0f;
       if (c < NG) v = sgs[hd * NG + c];
       else if (c >= NGP && c - NGP < r) v = us[hd * r + c - NGP];
-      v *= amul;
+      v *= amul(hd);
       hv[e] = used ? (lo ? f16_lo(v) : f16_hi(v)) : uint16_t(0);
     }
     baux[i] = make_uint2(pack_h2(hv[0], hv[1]), pack_h2(hv[2], hv[3]));
@@ -464,7 +511,7 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
           int qd = 0;
           if (hd < G) {
             const int c = 32 * g + 16 * hf + tig + 4 * i;
-            const int qi = __float2int_rn(qs[hd * D + c] * qmul);
+            const int qi = __float2int_rn(qs[hd * D + c] * qmul(hd));
             const int d1 = (qi + 128) >> 8;
             qd = dg ? d1 : qi - 256 * d1;
           }
@@ -642,8 +689,9 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
             for (int nt = 0; nt < NT; ++nt) {
               const int hd = 4 * nt + tig;
               if (hd < G) {
-                lg_s[t0 * LS + hd] = fmaf(L[nt][0], qinv, (Ca[nt][0] + Ca[nt][1]) * ainv);
-                lg_s[t1 * LS + hd] = fmaf(L[nt][1], qinv, (Ca[nt][2] + Ca[nt][3]) * ainv);
+                const int sc = APART ? nt : 0;
+                lg_s[t0 * LS + hd] = fmaf(L[nt][0], qinv[sc], (Ca[nt][0] + Ca[nt][1]) * ainv[sc]);
+                lg_s[t1 * LS + hd] = fmaf(L[nt][1], qinv[sc], (Ca[nt][2] + Ca[nt][3]) * ainv[sc]);
               }
             }
           }
@@ -860,9 +908,12 @@ __global__ void __launch_bounds__(kThreads) decode_split(SplitParams p) {
       for (int j = tile; j < issued; ++j) mbar_wait(bar0 + 8 * (j % kStages), (j / kStages) & 1, p.budget);
     }
     float* dst = p.part + (size_t(bh) * p.splits + split) * G * (D + 2);
-    // (the sum too: it reaches the merged row whatever the weight of this split)
-    for (int i = tid; i < G * (D + 2); i += kThreads)
-      dst[i] = i % (D + 2) == D ? 0.0f : __int_as_float(0x7fc00000);
+    // (ROWS: the sum too, which reaches the merged row whatever the weight of this
+    // split; decode_combine takes the channels at any weight)
+    for (int i = tid; i < G * (D + 2); i += kThreads) {
+      const int c = i % (D + 2);
+      dst[i] = (c == D + 1 && !ROWS) ? 1.0f : (c == D ? 0.0f : __int_as_float(0x7fc00000));
+    }
     return;
   }
   __syncthreads();
@@ -920,8 +971,8 @@ size_t split_smem(int M, int r) {
 template <int D, int G, bool U16, int GS>
 cudaError_t launch_split(const SplitParams& sp, int B, cudaStream_t s) {
   const size_t smem = split_smem<D, G, U16, GS>(sp.M, sp.r);
-  auto kern = sp.psac_fmt == 1 ? (sp.lens ? decode_split<D, G, U16, true, GS, true> : decode_split<D, G, U16, true, GS, false>)
-                               : (sp.lens ? decode_split<D, G, U16, false, GS, true> : decode_split<D, G, U16, false, GS, false>);
+  auto kern = sp.psac_fmt == 1 ? (sp.rows ? decode_split<D, G, U16, true, GS, true> : decode_split<D, G, U16, true, GS, false>)
+                               : (sp.rows ? decode_split<D, G, U16, false, GS, true> : decode_split<D, G, U16, false, GS, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   dim3 grid(sp.splits, B * sp.H_kv);

@@ -117,6 +117,8 @@ struct DecodeArgs {
   // for it only before copying a tile that reaches such a slot. INT32_MAX:
   // ordinary stream order.
   int wait_from = INT32_MAX;
+  // cross attention and shared prefixes: lengths from `lens`, heads scaled by themselves
+  bool rows = false;
   const int32_t* lens = nullptr;    // device [B]: tokens per sequence, taken into 0..len (null: len each)
   const int32_t* q_lens = nullptr;  // device [B]: sequences of no query (<= 0) are not written (null: all are)
 };

@@ -1485,6 +1485,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
   if (pl.splits) {
     float* part = reinterpret_cast<float*>(ws + pl.split);
     DecodeArgs d{a.src[1].c, a.src[1].max_len, a.H_q, a.Q, a.sm_scale, nullptr, a.out_dtype, a.ws, 0};
+    d.rows = true;
     d.lens = a.src[1].lens;
     p.split_part = part;
     p.splits = pl.splits;

@@ -462,8 +462,11 @@ size_t kv2_attention_cross_workspace_size(const kv2_cache* cache, int H_q, int N
  * scaled per row by a power of two (exact), (qP) rounded to fp16,
  * probabilities fp16 against a running maximum that may trail the true one by
  * a factor of 2^7. With Nq = 1 and H_q / H_kv in {1, 2, 4, 8}: the kernel and
- * the arithmetic of kv2_attention_decode. A row's result depends on no other
- * row; a query row that holds a NaN or an infinity gives NaN in its own row.
+ * the arithmetic of kv2_attention_decode, but each head's fixed-point query
+ * scaled by its own largest component. A row's result depends on no other row
+ * (on that kernel, beyond fp32 rounding: the query heads of a KV head move
+ * their running maxima together); a query row that holds a NaN or an infinity
+ * gives NaN in its own row.
  * ws     : device workspace of kv2_attention_cross_workspace_size bytes, its
  *          first 32-bit word zeroed by the caller before the first use: the
  *          kernel sets it to 1 when one of its waits runs out of its budget
@@ -504,7 +507,7 @@ size_t kv2_attention_shared_workspace_size(const kv2_cache* prefix, const kv2_ca
  * Q, out : bf16 [B][H_q][d]; fp32 or bf16 [B][H_q][d].
  * Requirements, arithmetic, replay and ws: as kv2_attention_cross (where
  * B * H_kv is more than the GPU's SMs and H_q / H_kv is 1, 2, 4 or 8, the own
- * caches take kv2_attention_decode's kernel and arithmetic).
+ * caches take its kernel for Nq = 1).
  * Errors: KV2_ERR_INVALID_ARG (cache->B not a multiple of prefix->B, different
  * H_kv or d, NULL or misaligned pointers), KV2_ERR_UNSUPPORTED (r; more than
  * 2^30 query rows), KV2_ERR_CAPACITY (a maximum beyond its cache),
