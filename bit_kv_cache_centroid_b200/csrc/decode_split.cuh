@@ -15,12 +15,12 @@
 //   out     = sum_t softmax_t * (code_t s_t + z_t)
 //
 // Two kernels:
-//   decode_split  grid (splits, B*H_kv), 4 warps. Prologue: the query-side
-//                 tables of the G query heads sharing the KV head (q in log2
-//                 units, q.mu_j for every centre, u = qP, per-group sums of q),
-//                 built while the first tile is in flight. Then 128-token tiles
-//                 of every packed stream arrive by 1-D bulk copies (three
-//                 stages, one barrier each) and each tile takes three phases:
+//   decode_split  grid (splits, B*H_kv), ROWS: their product; 4 warps. Prologue:
+//                 the query-side tables of the G query heads sharing the KV head
+//                 (q in log2 units, q.mu_j for every centre, u = qP, per-group
+//                 sums of q), built while the first tile is in flight. Then
+//                 128-token tiles of every packed stream arrive by 1-D bulk copies
+//                 (three stages, one barrier each) and each tile takes three phases:
 //                   q.k   the sums  sum_{c in g} q_c code_c  as 8-bit integer
 //                         MMAs (mma.sync m16n8k32, A = codes as u8, B = q as
 //                         two signed 8-bit digits, exact int32), scaled by the
@@ -283,7 +283,10 @@ __global__ void __launch_bounds__(kThreads, ROWS && G == 1 ? 6 : 0) decode_split
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, tig = lane & 3;
-  const int split = blockIdx.x, bh = blockIdx.y;
+  // (a grid's y ends at 65,535 pairs, 8,192 sequences of 8 heads; the division
+  // costs the plain kernel six registers and 1.5 % of the decode above)
+  const int split = ROWS ? int(blockIdx.x % unsigned(p.splits)) : int(blockIdx.x);
+  const int bh = ROWS ? int(blockIdx.x / unsigned(p.splits)) : int(blockIdx.y);
   const int b = bh / p.H_kv, h = bh % p.H_kv;
   const size_t base_slot = size_t(bh) * p.cap;
   const int t_begin = split * p.tiles_per_split * kTile;
@@ -971,11 +974,13 @@ size_t split_smem(int M, int r) {
 template <int D, int G, bool U16, int GS>
 cudaError_t launch_split(const SplitParams& sp, int B, cudaStream_t s) {
   const size_t smem = split_smem<D, G, U16, GS>(sp.M, sp.r);
-  auto kern = sp.psac_fmt == 1 ? (sp.rows ? decode_split<D, G, U16, true, GS, true> : decode_split<D, G, U16, true, GS, false>)
-                               : (sp.rows ? decode_split<D, G, U16, false, GS, true> : decode_split<D, G, U16, false, GS, false>);
+  const long long pairs = static_cast<long long>(B) * sp.H_kv;
+  const bool rows = sp.rows || pairs > 65535;       // what the plain kernel's grid does not hold
+  auto kern = sp.psac_fmt == 1 ? (rows ? decode_split<D, G, U16, true, GS, true> : decode_split<D, G, U16, true, GS, false>)
+                               : (rows ? decode_split<D, G, U16, false, GS, true> : decode_split<D, G, U16, false, GS, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  dim3 grid(sp.splits, B * sp.H_kv);
+  const dim3 grid = rows ? dim3(unsigned(sp.splits * pairs)) : dim3(unsigned(sp.splits), unsigned(pairs));
   if (sp.wait_from == INT32_MAX) {
     kern<<<grid, kThreads, smem, s>>>(sp);
     return cudaGetLastError();
