@@ -1,6 +1,7 @@
 // api.cu — extern "C" entry points of libkv2 (declared in include/kv2.h):
 // argument validation, workspace sizing and kernel dispatch. The library never
 // allocates device memory; every buffer is the caller's.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -410,6 +411,12 @@ kv2_status check_rows_cache(const char* what, const kv2_cache* c, const int32_t*
   return KV2_OK;
 }
 
+// (a row of scores that are not numbers would pass for one of equal weights)
+kv2_status check_rows_scale(const char* what, float sm_scale) {
+  if (!std::isfinite(sm_scale)) return fail(KV2_ERR_INVALID_ARG, "%s: sm_scale=%g", what, double(sm_scale));
+  return KV2_OK;
+}
+
 kv2_status check_rows_io(const char* what, const uint16_t* Q, const void* out, int out_dtype, const void* ws,
                          size_t ws_bytes, size_t need) {
   if (out_dtype != KV2_OUT_F32 && out_dtype != KV2_OUT_BF16)
@@ -466,6 +473,7 @@ kv2_status kv2_attention_cross(const kv2_cache* c, const int32_t* lens, int max_
                                void* ws, size_t ws_bytes, void* stream) {
   const CallRange range_("kv2_attention_cross");
   kv2_status st = check_rows_cache("cross", c, lens, max_len, H_q);
+  if (st == KV2_OK) st = check_rows_scale("cross", sm_scale);
   if (st != KV2_OK) return st;
   if (reinterpret_cast<uintptr_t>(q_lens) & 3u) return fail(KV2_ERR_INVALID_ARG, "cross: q_lens not 4-byte aligned");
   if (Nq < 0) return fail(KV2_ERR_INVALID_ARG, "cross: Nq=%d", Nq);
@@ -504,6 +512,7 @@ kv2_status kv2_attention_shared(const kv2_cache* pre, const int32_t* prefix_lens
   kv2_status st = check_rows_cache("shared prefix", pre, prefix_lens, max_prefix_len, H_q);
   if (st != KV2_OK) return st;
   st = check_rows_cache("shared", c, lens, max_len, H_q);
+  if (st == KV2_OK) st = check_rows_scale("shared", sm_scale);
   if (st != KV2_OK) return st;
   if (pre->H_kv != c->H_kv || pre->d != c->d)
     return fail(KV2_ERR_INVALID_ARG, "shared: prefix has %d heads of %d channels, the cache %d of %d", pre->H_kv, pre->d,

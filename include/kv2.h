@@ -509,9 +509,9 @@ size_t kv2_attention_shared_workspace_size(const kv2_cache* prefix, const kv2_ca
  * B * H_kv is more than the GPU's SMs and H_q / H_kv is 1, 2, 4 or 8, the own
  * caches take its kernel for Nq = 1).
  * Errors: KV2_ERR_INVALID_ARG (cache->B not a multiple of prefix->B, different
- * H_kv or d, NULL or misaligned pointers), KV2_ERR_UNSUPPORTED (r; more than
- * 2^30 query rows), KV2_ERR_CAPACITY (a maximum beyond its cache),
- * KV2_ERR_WORKSPACE.
+ * H_kv or d, NULL or misaligned pointers, a NaN or infinite sm_scale),
+ * KV2_ERR_UNSUPPORTED (r; more than 2^30 query rows), KV2_ERR_CAPACITY (a
+ * maximum beyond its cache), KV2_ERR_WORKSPACE.
  */
 kv2_status kv2_attention_shared(const kv2_cache* prefix, const int32_t* prefix_lens, int max_prefix_len,
                                 const kv2_cache* cache, const int32_t* lens, int max_len, const uint16_t* Q, int H_q,
