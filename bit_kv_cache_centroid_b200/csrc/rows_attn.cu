@@ -894,7 +894,8 @@ __global__ void __launch_bounds__(RCfg<D, WIDE>::kThreads, 1) rows_attn_kernel(c
       const int live = w.ql * G - w.rb * N;       // rows of the unit
       const bool row_ok = ru < live, warp_ok = ru - lane < live;
       const int jx = WIDE ? 0 : (x - t0) & 1;     // the group's first tile of the part
-      float m = -INFINITY, l = 0.0f, base = 0.0f, sc = 0.0f, nm = 0.0f;
+      // (a row whose first scores are not numbers does not move m: its p are NaN by nm)
+      float m = -INFINITY, l = 0.0f, base = 0.0f, sc = 0.0f, nm = __int_as_float(0x7fc00000);
       for (int jj = jx; jj < cnt; jj += WIDE ? 1 : 2, ++k) {
         dead |= !mbar_wait_or_abort(bar + B_SFULL + 8 * x, k & 1, p.budget, abort);
         fence_after_sync();
