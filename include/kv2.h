@@ -461,7 +461,13 @@ size_t kv2_attention_cross_workspace_size(const kv2_cache* cache, int H_q, int N
  * keys fp16(code*s + fp16(z + centroid)), values fp16(code*s + z), queries
  * scaled per row by a power of two (exact), (qP) rounded to fp16,
  * probabilities fp16 against a running maximum that may trail the true one by
- * a factor of 2^7. With Nq = 1 and H_q / H_kv in {1, 2, 4, 8}: the kernel and
+ * a factor of 2^7. Once the size of a row's maximum reaches 2^21 (in log2
+ * units; the keys' fp16 rounding moves such scores by some 2^9) its score
+ * differences are taken at 2^-i of theirs, 2^i the largest power of two not
+ * above that size / 2^20: tokens that the rounding does not tell apart share
+ * the weight more evenly than by exp, a difference of 2^-14 of the maximum
+ * still leaves the smaller 2^-64. A maximum beyond fp32's range gives NaN.
+ * With Nq = 1 and H_q / H_kv in {1, 2, 4, 8}: the kernel and
  * the arithmetic of kv2_attention_decode, but each head's fixed-point query
  * scaled by its own largest component. A row's result depends on no other row
  * (on that kernel, beyond fp32 rounding: the query heads of a KV head move
