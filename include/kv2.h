@@ -478,8 +478,8 @@ size_t kv2_attention_cross_workspace_size(const kv2_cache* cache, int H_q, int N
  *          kernel sets it to 1 when one of its waits runs out of its budget
  *          (KV2_WAIT_BUDGET_CYCLES); rows it had not finished are then NaN.
  *          Calls that share a workspace must not overlap.
- * Errors: KV2_ERR_INVALID_ARG (NULL or misaligned pointers, Nq < 0, H_q not a
- * multiple of H_kv, a NaN or infinite sm_scale), KV2_ERR_UNSUPPORTED (r; more
+ * Errors: KV2_ERR_INVALID_ARG (NULL or misaligned pointers, Nq < 0, a NaN or
+ * infinite sm_scale), KV2_ERR_UNSUPPORTED (r; H_q not a multiple of H_kv; more
  * than 2^30 query rows), KV2_ERR_CAPACITY (max_len), KV2_ERR_WORKSPACE.
  */
 kv2_status kv2_attention_cross(const kv2_cache* cache, const int32_t* lens, int max_len, const uint16_t* Q,
@@ -516,8 +516,8 @@ size_t kv2_attention_shared_workspace_size(const kv2_cache* prefix, const kv2_ca
  * caches take its kernel for Nq = 1).
  * Errors: KV2_ERR_INVALID_ARG (cache->B not a multiple of prefix->B, different
  * H_kv or d, NULL or misaligned pointers, a NaN or infinite sm_scale),
- * KV2_ERR_UNSUPPORTED (r; more than 2^30 query rows), KV2_ERR_CAPACITY (a
- * maximum beyond its cache), KV2_ERR_WORKSPACE.
+ * KV2_ERR_UNSUPPORTED (r; H_q not a multiple of H_kv; more than 2^30 query
+ * rows), KV2_ERR_CAPACITY (a maximum beyond its cache), KV2_ERR_WORKSPACE.
  */
 kv2_status kv2_attention_shared(const kv2_cache* prefix, const int32_t* prefix_lens, int max_prefix_len,
                                 const kv2_cache* cache, const int32_t* lens, int max_len, const uint16_t* Q, int H_q,
