@@ -451,6 +451,12 @@ def _need(name, t, shape, dtypes, device):
         raise ValueError(f"{name}: on {t.device}, expected {device}")
 
 
+def _need_ws(ws, device):
+    """A call's workspace, when passed: contiguous, on the call's device (its size is the library's to check)."""
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        _need("ws", ws, ws.shape, (ws.dtype,), device)
+
+
 _BITS16 = (torch.bfloat16, torch.int16)
 
 
@@ -500,6 +506,7 @@ def kv2_rotary_append(cache: Cache, rotary: Rotary, K: torch.Tensor, V: torch.Te
         _need("Q", Q, (cache.B, n_new, H_q, cache.d), _BITS16, dev)
     elif Q_out is not None:
         raise ValueError("Q_out without Q")
+    _need_ws(ws, dev)
     with _on(stream, dev):
         if Q is not None:
             Q_out = torch.zeros_like(Q) if Q_out is None else Q_out
@@ -510,7 +517,7 @@ def kv2_rotary_append(cache: Cache, rotary: Rotary, K: torch.Tensor, V: torch.Te
         d, r = cache.desc(), rotary.desc()
         _check(_get_lib().kv2_rotary_append(ctypes.byref(d), ctypes.byref(r), _ptr(K), _ptr(V), _ptr(Q), _ptr(Q_out), H_q,
                                             _ptr(positions), _ptr(start), _ptr(count), n_new, candidates, _ptr(ws),
-                                            ws.numel(), _stream(stream)))
+                                            ws.nbytes, _stream(stream)))
     return Q_out
 
 
@@ -553,12 +560,13 @@ def kv2_attention_cross(cache: Cache, lens, Q: torch.Tensor, sm_scale: float, ou
         if t is not None:
             _need(name, t, (B,), (torch.int32,), dev)
     max_len = cache.capacity if max_len is None else int(max_len)
+    _need_ws(ws, dev)
     with _on(stream, dev):
         need = kv2_attention_cross_workspace_size(cache, H_q, Nq, max_len) if ws is None else 0
         out, ws = _rows_call(Q, Q.shape, out_dtype, out, ws, need)
         d = cache.desc()
         _check(_get_lib().kv2_attention_cross(ctypes.byref(d), _ptr(lens), max_len, _ptr(Q), _ptr(q_lens), Nq, H_q,
-                                              float(sm_scale), _ptr(out), out_dtype, _ptr(ws), ws.numel(),
+                                              float(sm_scale), _ptr(out), out_dtype, _ptr(ws), ws.nbytes,
                                               _stream(stream)))
     return out
 
@@ -590,13 +598,14 @@ def kv2_attention_shared(prefix: Cache, prefix_lens, cache: Cache, lens, Q: torc
             _need(name, t, (n,), (torch.int32,), dev)
     max_prefix_len = prefix.capacity if max_prefix_len is None else int(max_prefix_len)
     max_len = cache.capacity if max_len is None else int(max_len)
+    _need_ws(ws, dev)
     with _on(stream, dev):
         need = kv2_attention_shared_workspace_size(prefix, cache, H_q, max_prefix_len, max_len) if ws is None else 0
         out, ws = _rows_call(Q, Q.shape, out_dtype, out, ws, need)
         p, d = prefix.desc(), cache.desc()
         _check(_get_lib().kv2_attention_shared(ctypes.byref(p), _ptr(prefix_lens), max_prefix_len, ctypes.byref(d),
                                                _ptr(lens), max_len, _ptr(Q), H_q, float(sm_scale), _ptr(out),
-                                               out_dtype, _ptr(ws), ws.numel(), _stream(stream)))
+                                               out_dtype, _ptr(ws), ws.nbytes, _stream(stream)))
     return out
 
 
