@@ -158,9 +158,17 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# (the current stream's handle alone: a Stream object costs 3 us of a short call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
-    # (the handle alone: a Stream object costs 3 us of a short call)
-    s = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _raw_stream is not None:
+        s = _raw_stream(torch.cuda.current_device())
+    else:                                       # a PyTorch without that name
+        s = torch.cuda.current_stream().cuda_stream
     return ctypes.c_void_p(s)
 
 
