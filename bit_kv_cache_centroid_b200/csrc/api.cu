@@ -226,10 +226,11 @@ kv2::QuantizeArgs quantize_args(const kv2_cache* c, const uint16_t* K, const uin
   return a;
 }
 
-// rows of a rotary append are ints in the kernels
+// rows of a rotary append are ints in the kernels, and so are a token's query channels
 bool rotary_too_many(const kv2_cache* c, int n_new, int H_q) {
   const long long rows = static_cast<long long>(c->B) * n_new;
-  return rows > (1ll << 30) || rows * c->H_kv > (1ll << 30) || rows * H_q > (1ll << 40);
+  return rows > (1ll << 30) || rows * c->H_kv > (1ll << 30) || rows * H_q > (1ll << 40) ||
+         static_cast<long long>(H_q) * c->d > (1ll << 30);
 }
 
 // argument checks of a decode call (the cache already checked)
@@ -304,7 +305,8 @@ kv2_status kv2_rotary_append(const kv2_cache* c, const kv2_rotary* rot, const ui
     return fail(KV2_ERR_INVALID_ARG, "rotary: candidates=%d outside 1..M=%d", candidates, c->M);
   if (Q && H_q <= 0) return fail(KV2_ERR_INVALID_ARG, "rotary: H_q=%d", H_q);
   if (rotary_too_many(c, n_new, Q ? H_q : 1))
-    return fail(KV2_ERR_UNSUPPORTED, "rotary: B=%d x n_new=%d tokens above 2^30 rows", c->B, n_new);
+    return fail(KV2_ERR_UNSUPPORTED, "rotary: B=%d x n_new=%d tokens above 2^30 rows, or H_q=%d x d above 2^30", c->B,
+                n_new, H_q);
   if (n_new == 0) return ok();
   if (!rot->cos_sin || !aligned16(rot->cos_sin))
     return fail(KV2_ERR_INVALID_ARG, "rotary: cos_sin NULL or not 16-byte aligned");

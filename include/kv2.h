@@ -283,7 +283,8 @@ size_t kv2_rotary_append_workspace_size(const kv2_cache* cache, int n_new);
  *            first 32-bit word zeroed by the caller before the first use.
  *            Calls that share a workspace must not overlap.
  * Errors: those of kv2_quantize_append's cache and candidates;
- * KV2_ERR_UNSUPPORTED (rot odd or outside 2..d, more than 2^30 rows),
+ * KV2_ERR_UNSUPPORTED (rot odd or outside 2..d, more than 2^30 rows of keys, or
+ * more than 2^30 query channels a token),
  * KV2_ERR_INVALID_ARG (NULL or misaligned pointers), KV2_ERR_WORKSPACE.
  */
 kv2_status kv2_rotary_append(const kv2_cache* cache, const kv2_rotary* rotary, const uint16_t* K, const uint16_t* V,
