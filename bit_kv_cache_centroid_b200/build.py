@@ -5,6 +5,7 @@
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -29,6 +30,18 @@ def _newer(src_paths, target):
     return any(os.path.getmtime(p) > t for p in src_paths)
 
 
+# Registers per thread that a kernel trades between its warps at run time
+# (``RCfg::kRegs`` in rows_attn.cu): its launch refuses any other number.
+TRADED = {"rows_attn.cu": ("rows_attn_kernel", 72)}
+
+
+def wrong_registers(src: str, log: str) -> list:
+    """(kernel, registers) of ptxas -v's log whose number is not the traded one."""
+    name, want = TRADED[src]
+    used = re.findall(r"Compiling entry function '([^']*)'.*?Used (\d+) registers", log, re.S)
+    return [(k, int(n)) for k, n in used if name in k and int(n) != want]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
@@ -40,14 +53,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         if force or _newer([sp] + headers, obj):
             cmd = [NVCC, "-c", sp, "-o", obj + ".tmp"] + FLAGS
-            if verbose:
+            if verbose or src in TRADED:
                 cmd += ["-Xptxas", "-v"]
+            if verbose:
                 print(" ".join(cmd), flush=True)
-            jobs.append((cmd, obj))
+            jobs.append((cmd, src, obj))
 
     def compile_one(job):
-        cmd, obj = job
-        subprocess.run(cmd, check=True)
+        cmd, src, obj = job
+        if src in TRADED:
+            r = subprocess.run(cmd, stderr=subprocess.PIPE, text=True)
+            if verbose or r.returncode:
+                print(r.stderr, file=sys.stderr, flush=True)
+            r.check_returncode()
+            for kernel, n in wrong_registers(src, r.stderr):
+                print(f"warning: {src}: {kernel} takes {n} registers, its role split {TRADED[src][1]}: "
+                      "its calls will return KV2_ERR_CUDA", file=sys.stderr, flush=True)
+        else:
+            subprocess.run(cmd, check=True)
         os.replace(obj + ".tmp", obj)
 
     # the translation units are independent: compile them side by side
