@@ -60,9 +60,9 @@
 // for the softmax warps of the group, which arrive no more once their own wait
 // has failed.
 //
-// Measured on a B200 (cold caches): 4,680 queries x 4,096 keys x 40 heads 765 us,
-// 530 TFLOP/s, 0.32 of the bf16 GEMM rate; x 512 keys 152 us; 32 rows (8
-// continuations of 4 heads) over 32,768 shared keys 64 us. Bound: the softmax
+// Measured on a B200 (cold caches): 4,680 queries x 4,096 keys x 40 heads 759 us,
+// 533 TFLOP/s, 0.32 of the bf16 GEMM rate; x 512 keys 153 us; 32 rows (8
+// continuations of 4 heads) over 32,768 shared keys 65 us. Bound: the softmax
 // and the hand-overs between the roles. A tile takes about 8,300 cycles for two
 // groups of 128 rows (softmax 4,000, of them 2,048 the exponentials; tensor core
 // 2,100) and 5,000 with up to 128 rows (keys 2,900), a unit 20,000 more for its
@@ -145,8 +145,8 @@ struct RCfg {
   // stages of keys, values and packed tiles. One of keys is enough: with WIDE
   // units the keys of tile t + 1 are multiplied a softmax after they could first
   // be written, else the scores' columns are free as late. A third packed tile
-  // hides the copies' latency instead (up to 128 rows over 32,768 keys: 59 us
-  // against 64 us with two stages of keys and two packed tiles).
+  // hides the copies' latency instead (128 rows over 32,768 keys, 8 KV heads: 61
+  // us against 65 us with two stages of keys and two packed tiles).
   static constexpr int KS = 1, VS = WIDE ? 1 : 2, RS = 3;
   // packed tile: codes of keys and values, scale and zero words, ids, PSAC
   // (fp16, or int8 codes and from RAW_PSC on the tokens' scales)
